@@ -98,6 +98,13 @@ extern "C" {
 #define QG_OP_GROUP_SUM_CORRECTION  3
 #define QG_OP_PACK                  4
 #define QG_OP_W4A16_SWIGLU          5
+#define QG_OP_FP8                   6
+#define QG_OP_MOE_SORT              7  /* M = tokens, N = topk, num_experts  */
+
+/* ---- element types, for the calls that take more than one ---- */
+#define QG_DTYPE_F16                0
+#define QG_DTYPE_BF16               1
+#define QG_DTYPE_F32                2
 
 /* 1 if HIP device `device` is a gfx950 GPU this library has kernels for,
  * else 0 (also 0 when the device does not exist).  The analogue of the pages'
@@ -303,6 +310,122 @@ int qgemm_w4a8(const int8_t *A_q, const float *a_scale, const uint32_t *w_packed
  * One kernel on `stream`. No workspace.                                     */
 int quantize_rows_int8(const uint16_t *A, int M, int K, int8_t *A_q, float *a_scale,
                        void *stream);
+
+/* ---- per-row, per-128-column fp8 quantization, the input stage of
+ *      qgemm_fp8 ----
+ * A        [M,K] fp16 or bf16 (dtype QG_DTYPE_F16 / QG_DTYPE_BF16)
+ *          activations, 16-byte aligned; K % 16 == 0 (else
+ *          QG_ERR_UNSUPPORTED).  With QG_QUANT_SWIGLU a [M,2K] gate/up pair
+ *          (gate columns first), and x below is silu(gate) * up in binary32;
+ *          without it x = A.
+ * A_q      [M,K] e4m3 codes out (OCP: largest value 448, no infinity),
+ *          16-byte aligned; a_scale [M, ceil(K/128)] fp32 out.  For each row
+ *          m and block b of 128 columns (the last may be partial):
+ *            a_scale[m,b] = max |x| / 448
+ *            A_q[m,k]     = e4m3(clamp(x[m,k] / a_scale[m,b], -448, 448))
+ *          both quotients single IEEE binary32 operations, the code rounded
+ *          to the nearest (ties to even).  A block of zeros gets scale 0 and
+ *          codes 0; a block with a NaN or an infinity gets a NaN scale and
+ *          NaN codes, so every product with it is NaN.
+ * M == 0 is a call that does nothing.  One kernel on `stream`, no workspace. */
+#define QG_QUANT_SWIGLU 0x1u
+int quantize_rows_fp8(const void *A, int dtype, int M, int K, unsigned flags, uint8_t *A_q,
+                      float *a_scale, void *stream);
+
+/* ---- block-scaled fp8 GEMM, dense or grouped by expert ----
+ * A_q          [M_a,K] e4m3 codes, 16-byte aligned; a_scale [M_a, KB] fp32,
+ *              KB = ceil(K/128): one scale per row and 128 columns
+ *              (quantize_rows_fp8 makes both).
+ * a_rows       NULL: row m of C takes row m of A (M_a == M_total).  Else
+ *              DEVICE int32[M_total]: row m of C takes row a_rows[m] of A
+ *              (moe_sort_rows' row_token: a token's row is quantized and
+ *              stored once, however many experts read it).  Rows whose index
+ *              lies outside [0, M_a) get zeros.  M_a * K must stay below
+ *              2^32 - 256 (else QG_ERR_UNSUPPORTED).
+ * W            E stacked [N,K] e4m3 codes (k contiguous), 16-byte aligned;
+ *              w_scale E stacked [ceil(N/128), KB] fp32: one scale per 128 x
+ *              128 block.
+ * expert_offsets  as for qgemm_w4a8: DEVICE int32[E+1], non-decreasing, or
+ *              NULL for one expert that owns all rows.  Rows outside
+ *              [offsets[0], offsets[E]) are left as they were.  The counts
+ *              are read on the device: no bound on them is needed.
+ * C            [M_total,N] fp16 or bf16 (dtype) out, overwritten:
+ *                C[m,n] = sum_b a_scale[r,b] * w_scale_e[n/128,b] * P
+ *                P      = sum_{k in b} A_q[r,k] * W_e[n,k],  r = a_rows[m]
+ *              in fp32, one rounding at the end.  P comes from the e4m3
+ *              matrix instruction, which adds eight products of consecutive
+ *              k at a time, each cut to 2^-13 of the eight's largest power
+ *              of two.
+ * N >= 1 and K % 16 == 0 (the last block may be partial in both); K < 2^22,
+ * ceil(N/128) * KB < 2^29.  M_total == 0 does nothing.
+ * workspace/workspace_bytes: qg_workspace_bytes(QG_OP_FP8, M_total, N, K, 128,
+ *              E, 0) bytes, 256-byte aligned: 0 (NULL) for every shape.
+ * flags        must be 0.                                                   */
+int qgemm_fp8(const uint8_t *A_q, const float *a_scale, const int32_t *a_rows, int M_a,
+              const uint8_t *W, const float *w_scale, const int32_t *expert_offsets,
+              int num_experts, int M_total, int N, int K, int dtype, void *C, void *workspace,
+              size_t workspace_bytes, unsigned flags, void *stream);
+
+/* ---- routing to experts ----
+ * logits   [T,E] of dtype QG_DTYPE_F32, _F16 or _BF16; bias [E] fp32 or NULL.
+ * score    s[t,e] = softmax over e of logits[t,:], or with QG_ROUTE_SIGMOID
+ *          1 / (1 + exp(-logits[t,e])).
+ * choice   c[t,e] = s[t,e] + bias[e] (the bias balances the load: it takes
+ *          part in the choice, not in the weights).
+ * groups   n_group > 1: the experts stand in n_group runs of E / n_group; a
+ *          run's value is its largest choice, or with QG_ROUTE_GROUP_TOP2 the
+ *          sum of its two largest; only experts of the topk_group runs with
+ *          the largest values can be chosen.
+ * ids      [T,topk] int32 out: the experts with the largest choices, largest
+ *          first.  Choices and sums rank in 64 bits; without a bias the
+ *          logits themselves rank the experts, and by their largest the
+ *          groups (the order of the scores, also where those saturate).
+ *          Equal ones go to the lowest index.
+ * weights  [T,topk] fp32 out: s[t,ids], with QG_ROUTE_RENORMALIZE divided by
+ *          their sum over the token's chosen experts, times `scaling`.
+ * An expert whose logit is -infinity or NaN, or whose choice is, is masked: it
+ * is never chosen, and slots left over hold id -1 and weight 0 (moe_sort_rows
+ * drops them).  A logit of +infinity counts as the largest, in equal shares.
+ * 1 <= E <= 1024, n_group <= 64 a divisor of E, 1 <= topk_group <= n_group,
+ * 1 <= topk <= 64 and <= topk_group * E / n_group.  T == 0 does nothing.  One
+ * kernel, no workspace.                                                     */
+#define QG_ROUTE_SIGMOID        0x1u
+#define QG_ROUTE_RENORMALIZE    0x2u
+#define QG_ROUTE_GROUP_TOP2     0x4u
+int moe_route(const void *logits, int dtype, const float *bias, int T, int E, int topk,
+              int n_group, int topk_group, float scaling, unsigned flags, int32_t *ids,
+              float *weights, void *stream);
+
+/* ---- the routed slots, sorted by expert ----
+ * ids      [T,topk] int32: the expert of each slot; ids outside [0,E) drop
+ *          their slot.
+ * The kept slots, ordered by expert and inside an expert by slot (t * topk +
+ * j), become the rows 0 .. M-1 of a grouped product, M = expert_offsets[E]:
+ * expert_offsets  [E+1] int32 out: expert e owns rows offsets[e] ..
+ *          offsets[e+1]-1 (as qgemm_w4a8 and qgemm_fp8 take them).
+ * row_token  [T*topk] int32 out: the token of each row; entries from M on are
+ *          left as they were.
+ * slot_row   [T,topk] int32 out: each slot's row, -1 for a dropped slot.
+ * T * topk < 2^30, 1 <= E <= 1024.  T == 0 writes expert_offsets = 0.
+ * workspace/workspace_bytes: qg_workspace_bytes(QG_OP_MOE_SORT, T, topk, 0, 0,
+ *          E, 0) bytes, 256-byte aligned (NULL when 0: few slots).  It needs
+ *          no initial value and keeps none between calls; its first
+ *          QG_W4A16_WS_COUNTER_BYTES bytes are never touched.              */
+int moe_sort_rows(const int32_t *ids, int T, int topk, int num_experts, int32_t *expert_offsets,
+                  int32_t *row_token, int32_t *slot_row, void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+/* ---- the experts' rows, weighted and summed back to their tokens ----
+ * Y        [M_rows,N] fp16 or bf16 (dtype); slot_row [T,topk] int32 from
+ *          moe_sort_rows; weights [T,topk] fp32 from moe_route.
+ * out      [T,N] of Y's type, overwritten:
+ *            out[t,n] = sum_j weights[t,j] * Y[slot_row[t,j], n]
+ *          in fp32 in the order of j, one rounding at the end.  A slot whose
+ *          row lies outside [0, M_rows) adds nothing, whatever its weight; a
+ *          token with no slot left gets zeros.
+ * 1 <= topk <= 64.  T == 0 does nothing.  One kernel, no workspace.         */
+int moe_combine_rows(const void *Y, int dtype, const int32_t *slot_row, const float *weights,
+                     int T, int topk, int M_rows, int N, void *out, void *stream);
 
 #ifdef __cplusplus
 }

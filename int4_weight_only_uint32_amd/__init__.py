@@ -8,10 +8,11 @@ computation runs in the library's HIP kernels; there is no fallback of any
 kind -- if libqgemm.so is missing, importing works but every call raises.
 
 Names follow the C ABI: pack_int4_weights, qgemm_w4a16, qgemm_w4a16_noalloc,
-qgemm_w4a16_swiglu, group_sum_correction, quantize_rows_int8, qgemm_w4a8 (plus
+qgemm_w4a16_swiglu, group_sum_correction, quantize_rows_int8, qgemm_w4a8,
+quantize_rows_fp8, qgemm_fp8, moe_route, moe_sort_rows, moe_combine_rows (plus
 qg_device_supported, qg_workspace_bytes, qg_padded_shape); pack, w4a16,
-w4a16_swiglu, correct, quantize_rows and w4a8 are the same calls with
-torch-allocated outputs.
+w4a16_swiglu, correct, quantize_rows, w4a8, quantize_fp8, fp8_gemm, route,
+sort_rows and combine_rows are the same calls with torch-allocated outputs.
 """
 import ctypes
 import os
@@ -42,11 +43,23 @@ QG_OP_W4A8 = 2
 QG_OP_GROUP_SUM_CORRECTION = 3
 QG_OP_PACK = 4
 QG_OP_W4A16_SWIGLU = 5
+QG_OP_FP8 = 6
+QG_OP_MOE_SORT = 7
+
+QG_DTYPE_F16 = 0
+QG_DTYPE_BF16 = 1
+QG_DTYPE_F32 = 2
+
+QG_QUANT_SWIGLU = 0x1
+QG_ROUTE_SIGMOID = 0x1
+QG_ROUTE_RENORMALIZE = 0x2
+QG_ROUTE_GROUP_TOP2 = 0x4
 
 EXPORTED = ("qg_device_supported", "qg_status_string", "qg_last_error", "qg_workspace_bytes",
             "pack_int4_weights", "qgemm_w4a16", "group_sum_correction", "qgemm_w4a8",
             "quantize_rows_int8", "qgemm_w4a16_swiglu", "qg_padded_shape",
-            "qgemm_w4a16_noalloc")
+            "qgemm_w4a16_noalloc", "quantize_rows_fp8", "qgemm_fp8", "moe_route", "moe_sort_rows",
+            "moe_combine_rows")
 
 
 class QGemmError(RuntimeError):
@@ -108,6 +121,16 @@ def open_library(path):
     L.qgemm_w4a16_swiglu.argtypes = [P, P, P, P, P, I, I, I, I, U, P, Z, P]
     L.quantize_rows_int8.restype = I
     L.quantize_rows_int8.argtypes = [P, I, I, P, P, P]
+    L.quantize_rows_fp8.restype = I
+    L.quantize_rows_fp8.argtypes = [P, I, I, I, U, P, P, P]
+    L.qgemm_fp8.restype = I
+    L.qgemm_fp8.argtypes = [P, P, P, I, P, P, P, I, I, I, I, I, P, P, Z, U, P]
+    L.moe_route.restype = I
+    L.moe_route.argtypes = [P, I, P, I, I, I, I, I, ctypes.c_float, U, P, P, P]
+    L.moe_sort_rows.restype = I
+    L.moe_sort_rows.argtypes = [P, I, I, I, P, P, P, P, Z, P]
+    L.moe_combine_rows.restype = I
+    L.moe_combine_rows.argtypes = [P, I, P, P, I, I, I, I, P, P]
     return L
 
 
@@ -380,3 +403,190 @@ def w4a16_swiglu(A: torch.Tensor, pair: PackedWeight, H: Optional[torch.Tensor] 
             workspace = workspace_for(A.device, n)
     qgemm_w4a16_swiglu(A, pair.w, pair.scale, pair.delta, H, M, N, K, pair.group_size, 0, workspace)
     return H
+
+
+# The calls below check shapes exactly and run on the current stream of their
+# first tensor's device, whichever device is current.
+
+_DTYPES = {torch.float16: QG_DTYPE_F16, torch.bfloat16: QG_DTYPE_BF16, torch.float32: QG_DTYPE_F32}
+
+
+def _dtype(t: torch.Tensor, name: str, f32=False) -> int:
+    code = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None or (code == QG_DTYPE_F32 and not f32):
+        raise TypeError(f"{name} must be {'fp32, ' if f32 else ''}fp16 or bf16")
+    return code
+
+
+def _arg(t: Optional[torch.Tensor], dtype, shape, device, name):
+    """A device tensor of this type, shape and device, contiguous; its pointer."""
+    if t is None:
+        return None
+    p = _ptr(t, dtype, name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return p
+
+
+def _call(fn, device, *args):
+    """fn(*args, stream) on `device`'s current stream; the library launches on
+    the current device, so another one is made current for the call."""
+    st = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, st)
+    _check(rc)
+
+
+def _blocks128(n: int) -> int:
+    return -(-n // 128)
+
+
+def quantize_rows_fp8(A, M, K, flags, A_q, a_scale):
+    """Same arguments as the C entry point; A [M,K] (or, QG_QUANT_SWIGLU,
+    [M,2K]) fp16 or bf16, A_q float8_e4m3fn, a_scale fp32."""
+    d = _dtype(A, "A")
+    pair = 2 if flags & QG_QUANT_SWIGLU else 1
+    dev = A.device
+    _call(lib().quantize_rows_fp8, dev, _arg(A, None, (M, pair * K), dev, "A"), d, M, K, flags,
+          _arg(A_q, torch.float8_e4m3fn, (M, K), dev, "A_q"),
+          _arg(a_scale, torch.float32, (M, _blocks128(K)), dev, "a_scale"))
+
+
+def quantize_fp8(A: torch.Tensor, swiglu: bool = False, A_q: Optional[torch.Tensor] = None,
+                 a_scale: Optional[torch.Tensor] = None):
+    """e4m3 codes [M,K] and fp32 scales [M, ceil(K/128)] (one per row and 128
+    columns) of fp16 or bf16 rows [M,K]; swiglu: of silu(gate) * up of a
+    [M,2K] gate/up pair."""
+    M, K = A.shape
+    if swiglu:
+        if K % 2:
+            raise ValueError(f"a gate/up pair has an even width, got {K}")
+        K //= 2
+    if A_q is None:
+        A_q = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=A.device)
+    if a_scale is None:
+        a_scale = torch.empty((M, _blocks128(K)), dtype=torch.float32, device=A.device)
+    quantize_rows_fp8(A, M, K, QG_QUANT_SWIGLU if swiglu else 0, A_q, a_scale)
+    return A_q, a_scale
+
+
+def qgemm_fp8(A_q, a_scale, a_rows, M_a, W, w_scale, expert_offsets, num_experts, M_total, N, K, C,
+              workspace=None, flags=0):
+    """Same arguments as the C entry point (dtype is C's); W [E,N,K] (or [N,K]
+    with one expert) float8_e4m3fn, w_scale [E, ceil(N/128), ceil(K/128)]."""
+    d = _dtype(C, "C")
+    dev, E, KB, NB = A_q.device, num_experts, _blocks128(K), _blocks128(N)
+    one = W.dim() == 2
+    if one and E != 1:
+        raise ValueError(f"W holds one expert, not {E}")
+    _call(lib().qgemm_fp8, dev, _arg(A_q, torch.float8_e4m3fn, (M_a, K), dev, "A_q"),
+          _arg(a_scale, torch.float32, (M_a, KB), dev, "a_scale"),
+          _arg(a_rows, torch.int32, (M_total,), dev, "a_rows"), M_a,
+          _arg(W, torch.float8_e4m3fn, (N, K) if one else (E, N, K), dev, "W"),
+          _arg(w_scale, torch.float32, (NB, KB) if one else (E, NB, KB), dev, "w_scale"),
+          _arg(expert_offsets, torch.int32, (E + 1,), dev, "expert_offsets"), E, M_total, N, K, d,
+          _arg(C, None, (M_total, N), dev, "C"), _ptr(workspace, None, "workspace"),
+          0 if workspace is None else workspace.numel() * workspace.element_size(), flags)
+
+
+def fp8_gemm(A_q: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor,
+             expert_offsets: Optional[torch.Tensor] = None, a_rows: Optional[torch.Tensor] = None,
+             C: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Block-scaled fp8 GEMM: A . W^T for one weight [N,K], or, grouped, row m
+    of expert e's range of expert_offsets times W[e] of [E,N,K].  a_rows: row m
+    takes row a_rows[m] of A_q (row_token of sort_rows)."""
+    M_a, K = A_q.shape
+    E, N = (1, W.shape[0]) if W.dim() == 2 else (W.shape[0], W.shape[1])
+    M = M_a if a_rows is None else a_rows.shape[0]
+    if C is None:
+        C = torch.empty((M, N), dtype=dtype, device=A_q.device)
+    qgemm_fp8(A_q, a_scale, a_rows, M_a, W, w_scale, expert_offsets, E, M, N, K, C)
+    return C
+
+
+def moe_route(logits, bias, T, E, topk, n_group, topk_group, scaling, flags, ids, weights):
+    """Same arguments as the C entry point (dtype is the logits')."""
+    d = _dtype(logits, "logits", f32=True)
+    dev = logits.device
+    _call(lib().moe_route, dev, _arg(logits, None, (T, E), dev, "logits"), d,
+          _arg(bias, torch.float32, (E,), dev, "bias"), T, E, topk, n_group, topk_group, scaling, flags,
+          _arg(ids, torch.int32, (T, topk), dev, "ids"),
+          _arg(weights, torch.float32, (T, topk), dev, "weights"))
+
+
+def route(logits: torch.Tensor, topk: int, bias: Optional[torch.Tensor] = None, score: str = "softmax",
+          n_group: int = 1, topk_group: int = 1, group_score: str = "max", renormalize: bool = True,
+          scaling: float = 1.0, ids: Optional[torch.Tensor] = None,
+          weights: Optional[torch.Tensor] = None):
+    """The topk experts of each token by softmax or sigmoid scores (plus a
+    bias, inside the topk_group best of n_group groups, ranked by their "max"
+    or the sum of their "top2"), and their weights; see include/qgemm.h."""
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    if group_score not in ("max", "top2"):
+        raise ValueError(f"group_score must be 'max' or 'top2', got {group_score!r}")
+    T, E = logits.shape
+    if ids is None:
+        ids = torch.empty((T, topk), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, topk), dtype=torch.float32, device=logits.device)
+    flags = ((QG_ROUTE_SIGMOID if score == "sigmoid" else 0) | (QG_ROUTE_RENORMALIZE if renormalize else 0) |
+             (QG_ROUTE_GROUP_TOP2 if group_score == "top2" else 0))
+    moe_route(logits, bias, T, E, topk, n_group, topk_group, scaling, flags, ids, weights)
+    return ids, weights
+
+
+def moe_sort_rows(ids, T, topk, num_experts, expert_offsets, row_token, slot_row, workspace=None):
+    """Same arguments as the C entry point."""
+    dev = ids.device
+    _call(lib().moe_sort_rows, dev, _arg(ids, torch.int32, (T, topk), dev, "ids"), T, topk, num_experts,
+          _arg(expert_offsets, torch.int32, (num_experts + 1,), dev, "expert_offsets"),
+          _arg(row_token, torch.int32, (T * topk,), dev, "row_token"),
+          _arg(slot_row, torch.int32, (T, topk), dev, "slot_row"), _ptr(workspace, None, "workspace"),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
+
+
+def sort_rows(ids: torch.Tensor, num_experts: int, expert_offsets: Optional[torch.Tensor] = None,
+              row_token: Optional[torch.Tensor] = None, slot_row: Optional[torch.Tensor] = None):
+    """Routed slots [T,topk] in expert order: (expert_offsets [E+1], row_token
+    [T*topk], slot_row [T,topk]); entries of row_token behind the last row are
+    not written."""
+    T, topk = ids.shape
+    if expert_offsets is None:
+        expert_offsets = torch.empty((num_experts + 1,), dtype=torch.int32, device=ids.device)
+    if row_token is None:
+        row_token = torch.empty((T * topk,), dtype=torch.int32, device=ids.device)
+    if slot_row is None:
+        slot_row = torch.empty((T, topk), dtype=torch.int32, device=ids.device)
+    n = qg_workspace_bytes(QG_OP_MOE_SORT, T, topk, 0, 0, num_experts, 0)
+    # from torch's allocator on each call: nothing is kept in it, and calls on
+    # other streams or in graphs captured side by side get their own
+    ws = torch.empty(n, dtype=torch.uint8, device=ids.device) if n > 0 else None
+    moe_sort_rows(ids, T, topk, num_experts, expert_offsets, row_token, slot_row, ws)
+    return expert_offsets, row_token, slot_row
+
+
+def moe_combine_rows(Y, slot_row, weights, T, topk, M_rows, N, out):
+    """Same arguments as the C entry point (dtype is Y's)."""
+    d = _dtype(Y, "Y")
+    dev = Y.device
+    _call(lib().moe_combine_rows, dev, _arg(Y, None, (M_rows, N), dev, "Y"), d,
+          _arg(slot_row, torch.int32, (T, topk), dev, "slot_row"),
+          _arg(weights, torch.float32, (T, topk), dev, "weights"), T, topk, M_rows, N,
+          _arg(out, Y.dtype, (T, N), dev, "out"))
+
+
+def combine_rows(Y: torch.Tensor, slot_row: torch.Tensor, weights: torch.Tensor,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out[t] = sum_j weights[t,j] * Y[slot_row[t,j]]; slots with row -1 add nothing."""
+    M_rows, N = Y.shape
+    T, topk = slot_row.shape
+    if out is None:
+        out = torch.empty((T, N), dtype=Y.dtype, device=Y.device)
+    moe_combine_rows(Y, slot_row, weights, T, topk, M_rows, N, out)
+    return out

@@ -236,6 +236,40 @@ int w4a16_launch(const char *what, const W4A16Call &call, const uint16_t *A,
     return rc;
 }
 
+// Shape rules of the fp8 GEMM: rows of whole 16-byte chunks, and the kernels'
+// 32-bit offsets within a tile's rows and within one expert's scales.
+int check_fp8_shape(const char *what, int M, int N, int K)
+{
+    if (M < 0 || N < 1 || K < 1)
+        return fail(QG_ERR_INVALID_ARG, "%s: M >= 0, N >= 1, K >= 1 needed (got %d, %d, %d)", what, M, N, K);
+    if (K % 16 != 0)
+        return fail(QG_ERR_UNSUPPORTED, "%s: K must be a multiple of 16 (got %d)", what, K);
+    const long long KB = (K + 127ll) / 128, NB = (N + 127ll) / 128;
+    if (K >= (1 << 22) || KB * NB >= (1ll << 29) || (long long)M + N > 0x7FFFFF00ll ||
+        (long long)M * K > (1ll << 46))
+        return fail(QG_ERR_UNSUPPORTED, "%s: M=%d, N=%d, K=%d too large", what, M, N, K);
+    return QG_OK;
+}
+
+// Threads of one launch's grid along x: a 32-bit count.
+constexpr long long MAX_GRID_THREADS = 0xFFFFFFFFll;
+
+int check_dtype16(const char *what, int dtype)
+{
+    if (dtype != QG_DTYPE_F16 && dtype != QG_DTYPE_BF16)
+        return fail(QG_ERR_INVALID_ARG, "%s: dtype %d is neither QG_DTYPE_F16 nor QG_DTYPE_BF16", what, dtype);
+    return QG_OK;
+}
+
+int check_sort_shape(const char *what, int T, int topk, int E)
+{
+    if (T < 0 || topk < 1 || E < 1)
+        return fail(QG_ERR_INVALID_ARG, "%s: T >= 0, topk >= 1, E >= 1 needed (got %d, %d, %d)", what, T, topk, E);
+    if (E > 1024 || (long long)T * topk >= (1ll << 30))
+        return fail(QG_ERR_UNSUPPORTED, "%s: T=%d, topk=%d, E=%d too large", what, T, topk, E);
+    return QG_OK;
+}
+
 } // namespace
 
 extern "C" {
@@ -293,7 +327,6 @@ const char *qg_last_error(void) { return g_err; }
 size_t qg_workspace_bytes(int op, int M, int N, int K, int group_size, int num_experts,
                           unsigned flags)
 {
-    (void)num_experts;
     int g = group_size;
     switch (op) {
     case QG_OP_W4A16:
@@ -316,6 +349,12 @@ size_t qg_workspace_bytes(int op, int M, int N, int K, int group_size, int num_e
     case QG_OP_W4A8:
         if (check_shape_tail("qg_workspace_bytes", M < 1 ? 1 : M, N, K, &g) != QG_OK) return (size_t)-1;
         return qg::is_tail_shape(N, K, g) ? qg::w4a8_tail_workspace_bytes(M < 1 ? 1 : M, N, K, g) : 0;
+    case QG_OP_FP8:
+        if (check_fp8_shape("qg_workspace_bytes", M, N, K) != QG_OK) return (size_t)-1;
+        return 0;
+    case QG_OP_MOE_SORT:
+        if (check_sort_shape("qg_workspace_bytes", M, N, num_experts) != QG_OK) return (size_t)-1;
+        return qg::moe_sort_workspace_bytes(M, N, num_experts);
     case QG_OP_PACK:
         if (check_shape("qg_workspace_bytes", M < 1 ? 1 : M, N, K, &g) != QG_OK) return (size_t)-1;
         return 0;
@@ -539,6 +578,162 @@ int quantize_rows_int8(const uint16_t *A, int M, int K, int8_t *A_q, float *a_sc
     hipError_t e = qg::launch_quantize_rows_int8(A, M, K, A_q, a_scale, (hipStream_t)stream);
     rc = launch_status(e, "quantize_rows_int8", (hipStream_t)stream);
     if (rc == QG_OK) log_first("quantize_rows_int8 M=%d K=%d", M, K);
+    return rc;
+}
+
+int quantize_rows_fp8(const void *A, int dtype, int M, int K, unsigned flags, uint8_t *A_q,
+                      float *a_scale, void *stream)
+{
+    const char *const what = "quantize_rows_fp8";
+    int rc = check_dtype16(what, dtype);
+    if (rc) return rc;
+    if (M < 0 || K < 1)
+        return fail(QG_ERR_INVALID_ARG, "%s: M >= 0 and K >= 1 needed (got %d, %d)", what, M, K);
+    if (K % 16) return fail(QG_ERR_UNSUPPORTED, "%s: K must be a multiple of 16 (got %d)", what, K);
+    if ((long long)M * ((K + 127) / 128) * 8 > MAX_GRID_THREADS - 256)
+        return fail(QG_ERR_UNSUPPORTED, "%s: M=%d, K=%d too large", what, M, K);
+    if (flags & ~QG_QUANT_SWIGLU) return fail(QG_ERR_INVALID_ARG, "%s: unknown flags 0x%x", what, flags);
+    if (M == 0) return ok();
+    if (!A || !A_q || !a_scale) return fail(QG_ERR_INVALID_ARG, "%s: NULL A/A_q/a_scale", what);
+    if (!aligned(A, 16) || !aligned(A_q, 16) || !aligned(a_scale, 4))
+        return fail(QG_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+    if ((rc = check_device())) return rc;
+    const bool swiglu = (flags & QG_QUANT_SWIGLU) != 0;
+    rc = launch_status(qg::launch_quantize_rows_fp8(A, dtype, M, K, swiglu, A_q, a_scale, (hipStream_t)stream),
+                       what, (hipStream_t)stream);
+    if (rc == QG_OK)
+        log_first("%s M=%d K=%d %s%s", what, M, K, dtype == QG_DTYPE_BF16 ? "bf16" : "fp16",
+                  swiglu ? ", SwiGLU pair" : "");
+    return rc;
+}
+
+int qgemm_fp8(const uint8_t *A_q, const float *a_scale, const int32_t *a_rows, int M_a,
+              const uint8_t *W, const float *w_scale, const int32_t *expert_offsets,
+              int num_experts, int M_total, int N, int K, int dtype, void *C, void *workspace,
+              size_t workspace_bytes, unsigned flags, void *stream)
+{
+    const char *const what = "qgemm_fp8";
+    (void)workspace;
+    (void)workspace_bytes;
+    int rc = check_fp8_shape(what, M_total, N, K);
+    if (rc) return rc;
+    if ((rc = check_dtype16(what, dtype))) return rc;
+    if (num_experts < 1 || num_experts > 65535)
+        return fail(QG_ERR_INVALID_ARG, "%s: num_experts %d out of range", what, num_experts);
+    if (!expert_offsets && num_experts != 1)
+        return fail(QG_ERR_INVALID_ARG, "%s: expert_offsets is required when E > 1", what);
+    if (flags != 0) return fail(QG_ERR_INVALID_ARG, "%s: unknown flags 0x%x", what, flags);
+    if (M_total == 0) return ok();
+    if (M_a < 0 || (!a_rows && M_a != M_total))
+        return fail(QG_ERR_INVALID_ARG, "%s: M_a %d with M_total %d and %s a_rows", what, M_a, M_total,
+                    a_rows ? "an" : "no");
+    if (M_a == 0) return fail(QG_ERR_INVALID_ARG, "%s: a_rows needs at least one row of A", what);
+    if (!A_q || !a_scale || !W || !w_scale || !C)
+        return fail(QG_ERR_INVALID_ARG, "%s: NULL A_q/a_scale/W/w_scale/C", what);
+    if (!aligned(A_q, 16) || !aligned(a_scale, 4) || !aligned(W, 16) || !aligned(w_scale, 4) ||
+        !aligned(C, 2) || (a_rows && !aligned(a_rows, 4)) || (expert_offsets && !aligned(expert_offsets, 4)))
+        return fail(QG_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+    if (a_rows && (long long)M_a * K >= (1ll << 32) - 256)
+        return fail(QG_ERR_UNSUPPORTED, "%s: a_rows with M_a * K = %lld bytes of codes (32-bit offsets)", what,
+                    (long long)M_a * K);
+    if (qg::fp8_workgroups(expert_offsets != nullptr, num_experts, M_total, N, K) > MAX_GRID_THREADS / 512)
+        return fail(QG_ERR_UNSUPPORTED, "%s: M_total=%d, N=%d, E=%d too large for one launch", what, M_total, N,
+                    num_experts);
+    if ((rc = check_device())) return rc;
+    rc = launch_status(qg::launch_fp8(A_q, a_scale, a_rows, M_a, W, w_scale, expert_offsets, num_experts,
+                                      M_total, N, K, dtype, C, (hipStream_t)stream),
+                       what, (hipStream_t)stream);
+    if (rc == QG_OK && log_enabled()) {
+        char kern[160];
+        qg::describe_fp8(expert_offsets != nullptr, num_experts, M_total, N, K, kern, sizeof(kern));
+        log_first("%s experts=%d M_total=%d N=%d K=%d %s%s: %s", what, num_experts, M_total, N, K,
+                  dtype == QG_DTYPE_BF16 ? "bf16" : "fp16", a_rows ? ", rows by index" : "", kern);
+    }
+    return rc;
+}
+
+int moe_route(const void *logits, int dtype, const float *bias, int T, int E, int topk,
+              int n_group, int topk_group, float scaling, unsigned flags, int32_t *ids,
+              float *weights, void *stream)
+{
+    const char *const what = "moe_route";
+    if (dtype != QG_DTYPE_F32 && dtype != QG_DTYPE_F16 && dtype != QG_DTYPE_BF16)
+        return fail(QG_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
+    if (T < 0 || E < 1 || topk < 1)
+        return fail(QG_ERR_INVALID_ARG, "%s: T >= 0, E >= 1, topk >= 1 needed (got %d, %d, %d)", what, T, E, topk);
+    if (E > 1024 || topk > 64 || n_group > 64)
+        return fail(QG_ERR_UNSUPPORTED, "%s: E=%d, topk=%d, n_group=%d (at most 1024, 64, 64)", what, E, topk, n_group);
+    if (T > MAX_GRID_THREADS / 64 - 4) return fail(QG_ERR_UNSUPPORTED, "%s: T=%d too large for one launch", what, T);
+    if (n_group < 1 || E % n_group || topk_group < 1 || topk_group > n_group)
+        return fail(QG_ERR_INVALID_ARG, "%s: %d of %d groups of E=%d experts", what, topk_group, n_group, E);
+    if (topk > topk_group * (E / n_group))
+        return fail(QG_ERR_INVALID_ARG, "%s: topk=%d of %d experts that can be chosen", what, topk,
+                    topk_group * (E / n_group));
+    if (flags & ~(QG_ROUTE_SIGMOID | QG_ROUTE_RENORMALIZE | QG_ROUTE_GROUP_TOP2))
+        return fail(QG_ERR_INVALID_ARG, "%s: unknown flags 0x%x", what, flags);
+    if (T == 0) return ok();
+    if (!logits || !ids || !weights) return fail(QG_ERR_INVALID_ARG, "%s: NULL logits/ids/weights", what);
+    if (!aligned(logits, dtype == QG_DTYPE_F32 ? 4 : 2) || (bias && !aligned(bias, 4)) || !aligned(ids, 4) ||
+        !aligned(weights, 4))
+        return fail(QG_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+    int rc = check_device();
+    if (rc) return rc;
+    rc = launch_status(qg::launch_moe_route(logits, dtype, bias, T, E, topk, n_group, topk_group, scaling, flags,
+                                            ids, weights, (hipStream_t)stream),
+                       what, (hipStream_t)stream);
+    if (rc == QG_OK)
+        log_first("%s T=%d E=%d topk=%d groups=%d/%d %s%s", what, T, E, topk, topk_group, n_group,
+                  (flags & QG_ROUTE_SIGMOID) ? "sigmoid" : "softmax", bias ? ", bias" : "");
+    return rc;
+}
+
+int moe_sort_rows(const int32_t *ids, int T, int topk, int num_experts, int32_t *expert_offsets,
+                  int32_t *row_token, int32_t *slot_row, void *workspace, size_t workspace_bytes,
+                  void *stream)
+{
+    const char *const what = "moe_sort_rows";
+    int rc = check_sort_shape(what, T, topk, num_experts);
+    if (rc) return rc;
+    if (!expert_offsets || (T > 0 && (!ids || !row_token || !slot_row)))
+        return fail(QG_ERR_INVALID_ARG, "%s: NULL ids/expert_offsets/row_token/slot_row", what);
+    if (!aligned(ids, 4) || !aligned(expert_offsets, 4) || !aligned(row_token, 4) || !aligned(slot_row, 4))
+        return fail(QG_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+    const size_t need = qg::moe_sort_workspace_bytes(T, topk, num_experts);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return fail(QG_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, got %zu", what, need,
+                        workspace ? workspace_bytes : (size_t)0);
+        if (!aligned(workspace, 256))
+            return fail(QG_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", what);
+    }
+    if ((rc = check_device())) return rc;
+    rc = launch_status(qg::launch_moe_sort(ids, T, topk, num_experts, expert_offsets, row_token, slot_row,
+                                           need ? workspace : nullptr, (hipStream_t)stream),
+                       what, (hipStream_t)stream);
+    if (rc == QG_OK) log_first("%s T=%d topk=%d E=%d", what, T, topk, num_experts);
+    return rc;
+}
+
+int moe_combine_rows(const void *Y, int dtype, const int32_t *slot_row, const float *weights,
+                     int T, int topk, int M_rows, int N, void *out, void *stream)
+{
+    const char *const what = "moe_combine_rows";
+    int rc = check_dtype16(what, dtype);
+    if (rc) return rc;
+    if (T < 0 || topk < 1 || M_rows < 0 || N < 1)
+        return fail(QG_ERR_INVALID_ARG, "%s: T=%d, topk=%d, M_rows=%d, N=%d", what, T, topk, M_rows, N);
+    if (topk > 64 || (long long)T * topk >= (1ll << 30) || N > (1 << 28))
+        return fail(QG_ERR_UNSUPPORTED, "%s: T=%d, topk=%d, N=%d too large", what, T, topk, N);
+    if (T == 0) return ok();
+    if ((M_rows > 0 && !Y) || !slot_row || !weights || !out)
+        return fail(QG_ERR_INVALID_ARG, "%s: NULL Y/slot_row/weights/out", what);
+    if (!aligned(Y, 2) || !aligned(slot_row, 4) || !aligned(weights, 4) || !aligned(out, 2))
+        return fail(QG_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+    if ((rc = check_device())) return rc;
+    rc = launch_status(qg::launch_moe_combine(Y, dtype, slot_row, weights, T, topk, M_rows, N, out,
+                                              (hipStream_t)stream),
+                       what, (hipStream_t)stream);
+    if (rc == QG_OK) log_first("%s T=%d topk=%d N=%d", what, T, topk, N);
     return rc;
 }
 

@@ -25,6 +25,7 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 typedef int int4v __attribute__((ext_vector_type(4)));
+typedef int int8v __attribute__((ext_vector_type(8)));
 typedef unsigned int uint4v __attribute__((ext_vector_type(4)));
 typedef unsigned int uint2v __attribute__((ext_vector_type(2)));
 
@@ -42,6 +43,8 @@ __host__ __device__ inline int tile_k(int kq, int j, int p)
 
 __device__ inline float h2f(uint16_t b) { return (float)__builtin_bit_cast(_Float16, b); }
 __device__ inline uint16_t f2h(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
+__device__ inline float bf2f(uint16_t b) { return __builtin_bit_cast(float, (unsigned)b << 16); }
+__device__ inline uint16_t f2bf(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
 // Strictly negative binary16 (not -0.0, not NaN).
 __host__ __device__ inline bool f16_is_negative(uint16_t b)
@@ -239,6 +242,22 @@ __device__ inline int4v mfma_i8_k32(int a0, int a1, int b0, int b1, int4v c)
     const long a = (long)(((unsigned long)(unsigned)a1 << 32) | (unsigned)a0);
     const long b = (long)(((unsigned long)(unsigned)b1 << 32) | (unsigned)b0);
     return __builtin_amdgcn_mfma_i32_16x16x32_i8(a, b, c, 0, 0, 0);
+}
+
+// 16x16x128 e4m3 MFMA: 32 bytes of A and of B per lane, hardware block scales
+// off (the zero scale operands select the unscaled instruction).  Lane l holds row
+// (column) l % 16 of its operand; the product is right for any assignment of
+// the 128 k to the four lane groups that A and B share.
+// Precision, measured with one large and one small product: the products of
+// eight consecutive bytes of a lane are added after each is cut toward zero
+// to a multiple of 2^(e - 13), e the largest exponent sum among them; the sums of
+// the eights and the accumulator keep 24 bits.  On normally distributed data
+// that is 1e-4 of the result's size (rms), below the half step of an fp16 output
+// (2.4e-4 of a value) and far below a bf16 one's.  The exact alternative, codes
+// widened to fp16 for the 16-bit MFMA, has half the rate before the widening.
+__device__ inline float4v mfma_fp8(int8v a, int8v b, float4v c)
+{
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 
 } // namespace qg

@@ -7,6 +7,9 @@
 
 namespace qg {
 
+// element types (the values of the C ABI's QG_DTYPE_*)
+constexpr int QG_DT_F16 = 0, QG_DT_BF16 = 1, QG_DT_F32 = 2;
+
 // Padded shape of a pack: Kp (K up to a whole group, or to 128 for one group
 // per column, g == K), Np (N up to 128), gp (the group size in the padded
 // layout: g, or Kp when g == K).  Kp == K and Np == N for aligned shapes.
@@ -141,5 +144,29 @@ hipError_t noalloc_scratch(hipStream_t st, void **out);
 // 16-byte and Aq 8-byte aligned).
 hipError_t launch_quantize_rows_int8(const uint16_t *A, int M, int K, int8_t *Aq,
                                      float *a_scale, hipStream_t st);
+
+// Codes and per-128-column scales of rows (or, swiglu, of silu(gate) * up of
+// [M, 2K] rows); K % 16 == 0.
+hipError_t launch_quantize_rows_fp8(const void *A, int dtype, int M, int K, bool swiglu,
+                                    uint8_t *Aq, float *a_scale, hipStream_t st);
+
+// Block-scaled fp8 GEMM (arguments as qgemm_fp8's, M_total >= 1).
+hipError_t launch_fp8(const uint8_t *A, const float *a_scale, const int32_t *a_rows, int M_a,
+                      const uint8_t *W, const float *w_scale, const int32_t *offsets, int E, int M,
+                      int N, int K, int dtype, void *C, hipStream_t st);
+// Workgroups of the launch (the caller refuses what exceeds a grid).
+long long fp8_workgroups(bool grouped, int E, int M, int N, int K);
+void describe_fp8(bool grouped, int E, int M, int N, int K, char *buf, size_t n);
+
+// flags: QG_ROUTE_* of the C ABI.
+hipError_t launch_moe_route(const void *logits, int dtype, const float *bias, int T, int E,
+                            int topk, int n_group, int topk_group, float scaling, unsigned flags,
+                            int32_t *ids, float *weights, hipStream_t st);
+size_t moe_sort_workspace_bytes(int T, int topk, int E);
+hipError_t launch_moe_sort(const int32_t *ids, int T, int topk, int E, int32_t *offsets,
+                           int32_t *row_token, int32_t *slot_row, void *ws, hipStream_t st);
+hipError_t launch_moe_combine(const void *Y, int dtype, const int32_t *slot_row,
+                              const float *weights, int T, int topk, int M_rows, int N, void *out,
+                              hipStream_t st);
 
 } // namespace qg
