@@ -340,8 +340,8 @@ int quantize_rows_fp8(const void *A, int dtype, int M, int K, unsigned flags, ui
  *              DEVICE int32[M_total]: row m of C takes row a_rows[m] of A
  *              (moe_sort_rows' row_token: a token's row is quantized and
  *              stored once, however many experts read it).  Rows whose index
- *              lies outside [0, M_a) get zeros.  M_a * K must stay below
- *              2^32 - 256 (else QG_ERR_UNSUPPORTED).
+ *              lies outside [0, M_a) get zeros.  M_a * K must not exceed
+ *              2^32 - 2^23 (else QG_ERR_UNSUPPORTED).
  * W            E stacked [N,K] e4m3 codes (k contiguous), 16-byte aligned;
  *              w_scale E stacked [ceil(N/128), KB] fp32: one scale per 128 x
  *              128 block.

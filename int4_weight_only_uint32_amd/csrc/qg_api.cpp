@@ -633,10 +633,10 @@ int qgemm_fp8(const uint8_t *A_q, const float *a_scale, const int32_t *a_rows, i
     if (!aligned(A_q, 16) || !aligned(a_scale, 4) || !aligned(W, 16) || !aligned(w_scale, 4) ||
         !aligned(C, 2) || (a_rows && !aligned(a_rows, 4)) || (expert_offsets && !aligned(expert_offsets, 4)))
         return fail(QG_ERR_INVALID_ARG, "%s: misaligned pointer", what);
-    if (a_rows && (long long)M_a * K >= (1ll << 32) - 256)
+    if (a_rows && (long long)M_a * K > (1ll << 32) - (1ll << 23))
         return fail(QG_ERR_UNSUPPORTED, "%s: a_rows with M_a * K = %lld bytes of codes (32-bit offsets)", what,
                     (long long)M_a * K);
-    if (qg::fp8_workgroups(expert_offsets != nullptr, num_experts, M_total, N, K) > MAX_GRID_THREADS / 512)
+    if (qg::fp8_threads(expert_offsets != nullptr, num_experts, M_total, N, K) > MAX_GRID_THREADS)
         return fail(QG_ERR_UNSUPPORTED, "%s: M_total=%d, N=%d, E=%d too large for one launch", what, M_total, N,
                     num_experts);
     if ((rc = check_device())) return rc;

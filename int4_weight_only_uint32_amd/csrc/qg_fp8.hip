@@ -17,27 +17,53 @@ namespace {
 
 constexpr int KB8 = 128;   // k extent of a scale block, bytes of a tile row
 
-// Rows of expert blocks.  The grid holds an upper bound on the number of
-// BM-row blocks over all experts; block rb of the list is found by a scan over
-// the offsets (64 experts a step, every wave for itself).
+// An offset past every buffer range here (at most 2^32 - 2^23 bytes, which the
+// caller checks), also after a step's scalar offset (below 2^22 + 256) is added.
+constexpr unsigned FP8_PAST = 0xFFBFFFF0u - 0x1000u;
+
+// The BM-row blocks of all experts, in order, and the one an index names.  The
+// counts stand in the device's offsets, so the grid is an upper bound and every
+// wave scans them for itself, 64 experts a step.
 struct RowBlock {
-    int e, m0, m1;      // expert, first row, end of the expert's rows; e < 0: none
+    int e, m0, m1;      // expert, first row, end of the expert's rows
 };
 
+__device__ inline void expert_rows(const int32_t *__restrict__ offsets, int E, int M, int e, int &r0,
+                                   int &r1)
+{
+    r0 = r1 = 0;
+    if (e < E) {
+        r0 = offsets[e];
+        r1 = offsets[e + 1];
+        r0 = r0 < 0 ? 0 : (r0 > M ? M : r0);
+        r1 = r1 < r0 ? r0 : (r1 > M ? M : r1);
+    }
+}
+
+__device__ inline int row_block_count(const int32_t *__restrict__ offsets, int E, int M, int BM)
+{
+    if (!offsets) return (M + BM - 1) / BM;
+    int n = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        int r0, r1;
+        expert_rows(offsets, E, M, e0 + (threadIdx.x & 63), r0, r1);
+        n += (r1 - r0 + BM - 1) / BM;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
+    return __builtin_amdgcn_readfirstlane(n);
+}
+
+// Row block rb of row_block_count's (rb below it).
 __device__ inline RowBlock find_rows(const int32_t *__restrict__ offsets, int E, int M, int BM,
                                      int rb)
 {
-    if (!offsets) return RowBlock{rb * BM < M ? 0 : -1, rb * BM, M};
+    if (!offsets) return RowBlock{0, rb * BM, M};
     const int lane = threadIdx.x & 63;
     int base = 0;
     for (int e0 = 0; e0 < E; e0 += 64) {
-        int r0 = 0, r1 = 0;
-        if (e0 + lane < E) {
-            r0 = offsets[e0 + lane];
-            r1 = offsets[e0 + lane + 1];
-            r0 = r0 < 0 ? 0 : (r0 > M ? M : r0);
-            r1 = r1 < r0 ? r0 : (r1 > M ? M : r1);
-        }
+        int r0, r1;
+        expert_rows(offsets, E, M, e0 + lane, r0, r1);
         const int nb = (r1 - r0 + BM - 1) / BM;
         int sum = nb;      // inclusive scan
 #pragma unroll
@@ -53,11 +79,45 @@ __device__ inline RowBlock find_rows(const int32_t *__restrict__ offsets, int E,
         }
         base += __shfl(sum, 63);
     }
-    return RowBlock{-1, 0, 0};
+    return RowBlock{0, 0, 0};
+}
+
+// The tile of workgroup b out of rbs row blocks x nbn column blocks, false if
+// there is none.  Workgroups go to the eight XCDs in turn; each XCD takes a
+// contiguous run of the tiles, ordered in bands of GM row blocks, so that the
+// tiles an XCD computes at a time share both operands in its L2.
+template <int GM>
+__device__ inline bool tile_of(int b, int rbs, int nbn, int &rb, int &nb)
+{
+    const int tiles = rbs * nbn;
+    if (b >= tiles) return false;
+    const int x = b & 7, q = tiles >> 3, r = tiles & 7;
+    const int id = x * q + (x < r ? x : r) + (b >> 3);
+    const int band = id / (GM * nbn), in = id - band * (GM * nbn);
+    const int rows = rbs - band * GM < GM ? rbs - band * GM : GM;
+    nb = in / rows;
+    rb = band * GM + in - nb * rows;
+    return true;
 }
 
 template <bool BF16>
 __device__ inline uint16_t out16(float f) { return BF16 ? f2bf(f) : f2h(f); }
+
+// Four consecutive columns n .. n + 3 of a row; zeros for a row of no activations.
+template <bool BF16>
+__device__ inline void store4(uint16_t *c, float4v x, bool zero, int n, int N, bool wide)
+{
+    uint16_t h[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) h[r] = zero ? 0 : out16<BF16>(x[r]);
+    if (wide) {
+        if (n < N) *reinterpret_cast<uint2v *>(c) = uint2v{h[0] | (unsigned)h[1] << 16, h[2] | (unsigned)h[3] << 16};
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (n + r < N) c[r] = h[r];
+    }
+}
 
 // ---- tiled kernel ----
 // BM x BN tile per workgroup of WM x WN waves; each wave MT x NT 16 x 16
@@ -80,9 +140,11 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     constexpr int STAGE = (BM + BN) * KB8;
 
     const int nbn = (N + BN - 1) / BN;
-    const int rb = blockIdx.x / nbn, n0 = (blockIdx.x % nbn) * BN;
+    int rb, n0;
+    // uniform over the workgroup, before any barrier
+    if (!tile_of<1024 / BM>(blockIdx.x, row_block_count(offsets, E, M, BM), nbn, rb, n0)) return;
+    n0 *= BN;
     const RowBlock blk = find_rows(offsets, E, M, BM, rb);
-    if (blk.e < 0) return;      // uniform over the workgroup, before any barrier
     const int e = __builtin_amdgcn_readfirstlane(blk.e);
     const int m0 = __builtin_amdgcn_readfirstlane(blk.m0);
     const int m1 = __builtin_amdgcn_readfirstlane(blk.m1);
@@ -115,46 +177,48 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
         r = r < rows_n ? r : rows_n - 1;
         w_off[i] = (unsigned)r * (unsigned)K + chunk * 16;
     }
-    auto load = [&](int kt, int st) {
-        // past the end of K (last step of a K that is no multiple of 128) an
-        // offset beyond every range makes the load give zeros
+    // Every load of step kt.  Chunks past the end of K (in the last step of a
+    // K that is no multiple of 128, and in the steps past the last that the loop
+    // below asks for without a branch) take an offset beyond every range, which
+    // the step's scalar offset cannot wrap: such loads give zeros and read
+    // nothing.
+    // (plain variables of a fixed type: a target builtin given an argument
+    // whose type depends on a template parameter loses the kernel's host
+    // launch stub)
+    constexpr int PIECES = LA + LW;
+    auto load_piece = [&](int kt, int q) {
         const bool in = kt * KB8 + chunk * 16 < K;
-        uint8_t *base = lds + st * STAGE;
-        // (plain variables of a fixed type: a target builtin given an argument
-        // whose type depends on a template parameter loses the kernel's host
-        // launch stub)
-#pragma unroll
-        for (int i = 0; i < LA; ++i) {
-            const unsigned off = in ? a_off[i] + kt * KB8 : 0xFFFFFFF0u;
-            uint8_t *dst = base + (wave * LA + i) * 1024;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rs, (__attribute__((address_space(3))) void *)dst, 16, off, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < LW; ++i) {
-            const unsigned off = in ? w_off[i] + kt * KB8 : 0xFFFFFFF0u;
-            uint8_t *dst = base + BM * KB8 + (wave * LW + i) * 1024;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rs, (__attribute__((address_space(3))) void *)dst, 16, off, 0, 0, 0);
-        }
+        unsigned off = in ? (q < LA ? a_off[q] : w_off[q - LA]) : FP8_PAST;
+        pin(off);        // one load for all lanes, not two under half an exec mask
+        uint8_t *dst = lds + (kt & 1) * STAGE + (q < LA ? wave * LA + q : BM / 8 + wave * LW + q - LA) * 1024;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(q < LA ? a_rs : w_rs, (__attribute__((address_space(3))) void *)dst, 16, off, kt * KB8, 0, 0);
     };
 
-    // scales: a lane's row of each m-tile, the wave's weight block
-    const float *srow[MT];
+    // Scales, four steps at a time: lane l loads, for its row (l % 16) of each
+    // m-tile, the scale of step 4 c + l / 16, so one 4-byte load a row serves
+    // four steps (a load for every step asks L2 for a whole line per row each
+    // time: 52 of 278 us at 4096 x 8192 x 8192).  The product with the
+    // weight block's scale is then handed to the four lanes of a row by a
+    // lane permute.
+    unsigned s_off[MT];
     bool bad[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        int r = m0 + (wm * MT + t) * 16 + (lane & 15);
-        r = r < m1 ? r : m1 - 1;
+        int r = (wm * MT + t) * 16 + (lane & 15);
+        r = m0 + r < m1 ? r : m1 - 1 - m0;
         bad[t] = false;
         if (a_rows) {
-            r = a_rows[r];
+            r = a_rows[m0 + r];
             bad[t] = (unsigned)r >= (unsigned)M_a;
             r = bad[t] ? 0 : r;
         }
-        srow[t] = a_scale + (size_t)r * KB;
+        s_off[t] = ((unsigned)r * (unsigned)KB + (lane >> 4)) * 4u;
     }
+    const __amdgpu_buffer_rsrc_t sa_rs = a_rows ? buffer_rsrc(a_scale, (size_t)M_a * KB * 4)
+                                                : buffer_rsrc(a_scale + (size_t)m0 * KB, (size_t)(m1 - m0) * KB * 4);
     int nb = (n0 + wn * NT * 16) / 128;
     nb = nb < NB ? nb : NB - 1;
-    const float *sw = Sall + ((size_t)e * NB + nb) * KB;
+    const __amdgpu_buffer_rsrc_t sw_rs = buffer_rsrc(Sall + ((size_t)e * NB + nb) * KB, (size_t)KB * 4);
 
     float4v acc[MT][NT];
 #pragma unroll
@@ -165,45 +229,118 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     // operand position of this lane in a 16-row tile: chunks q and q ^ 4 of
     // lane group q = lane / 16
     const int o0 = (lane & 15) * KB8 + (((lane >> 4) ^ (lane & 7)) * 16);
-    float sa[MT], sb = sw[0];      // the step's scales, loaded one step ahead
+    const int a_base = wm * MT * 16 * KB8, w_base = (BM + wn * NT * 16) * KB8;
+    auto operand = [&](int pos) {      // byte position of a 16-row tile in LDS
+        const int4v lo = *reinterpret_cast<const int4v *>(lds + pos + o0);
+        const int4v hi = *reinterpret_cast<const int4v *>(lds + pos + (o0 ^ 64));
+        return int8v{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    };
+
+    // Schedule.  One wave's MFMAs follow each other without a pause only if
+    // nothing it issues in between waits: the FMAs that fold a product run two
+    // MFMAs behind it (ring of four products), the next column tile's operand is
+    // read a column tile ahead, and the step's one barrier stands before its last
+    // column tile.  There every operand of the step is in registers, so behind it
+    // the step's buffer is filled again (for step k + 2), step k + 1's tiles have
+    // landed, and its first operands are read between the last MFMAs.  The
+    // scheduling barriers keep this order.
+    float sa[MT], sb;             // scales of the next four steps, in flight
+    float four[MT];               // products of the scales of four steps
+    float s[MT], s_old[MT];       // this step's, and those of the step whose last results wait
+    float4v p[4];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) sa[t] = srow[t][0];
-    load(0, 0);
-    for (int kt = 0; kt < KB; ++kt) {
-        // this step's tiles have landed, and every wave has read the last step's
-        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
-        __syncthreads();
-        float s[MT];
+    for (int t = 0; t < 4; ++t) p[t] = float4v{0.f, 0.f, 0.f, 0.f};
+    // (no branch: where `now` is false the loads read nothing)
+    auto load_scales = [&](int c, bool now) {
+        unsigned off = now ? (unsigned)(lane >> 4) * 4u : FP8_PAST;
+        pin(off);
+        sb = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sw_rs, off, c * 16, 0));
 #pragma unroll
-        for (int t = 0; t < MT; ++t) s[t] = sa[t] * sb;
-        if (kt + 1 < KB) {
-            sb = sw[kt + 1];
-#pragma unroll
-            for (int t = 0; t < MT; ++t) sa[t] = srow[t][kt + 1];
-            load(kt + 1, (kt + 1) & 1);
+        for (int t = 0; t < MT; ++t) {
+            unsigned o = now ? s_off[t] : FP8_PAST;
+            pin(o);
+            sa[t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sa_rs, o, c * 16, 0));
         }
-        const uint8_t *At = lds + (kt & 1) * STAGE + wm * MT * 16 * KB8;
-        const uint8_t *Wt = lds + (kt & 1) * STAGE + (BM + wn * NT * 16) * KB8;
-        auto operand = [&](const uint8_t *p) {
-            const int4v lo = *reinterpret_cast<const int4v *>(p + o0);
-            const int4v hi = *reinterpret_cast<const int4v *>(p + (o0 ^ 64));
-            return int8v{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        };
-        int8v a[MT];
+    };
+    auto of_step = [&](float x, int kt) {     // the value of lane group kt % 4
+        const int from = ((kt & 3) * 16 + (lane & 15)) * 4;
+        return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, x)));
+    };
+    load_scales(0, true);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) a[i] = operand(At + i * 16 * KB8);
+    for (int q = 0; q < PIECES; ++q) load_piece(0, q);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        four[t] = sa[t] * sb;
+        s[t] = of_step(four[t], 0);
+        s_old[t] = 0.f;
+    }
+    // Loads are spread over the MFMAs of half a step, one after every GAP of
+    // them: a burst of all of them behind the barrier holds every wave's issue
+    // until the address unit has taken them.  Slot i of the last column tile and
+    // slot (j + 1) * MT + i of column tile j of the next step.
+    constexpr int GAP = NT / 2 * MT / PIECES > 0 ? NT / 2 * MT / PIECES : 1;
+    static_assert(GAP * PIECES <= NT * MT, "every load has a slot");
+#pragma unroll
+    for (int i = 0; i < MT; i += GAP)
+        if (i / GAP < PIECES) load_piece(1, i / GAP);
+    int8v a[MT], w[2];
+    w[0] = operand(w_base);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) a[i] = operand(a_base + i * 16 * KB8);
+    static_assert(NT % 2 == 0 && MT * NT % 4 == 0, "rings of two operands and four products");
+
+    for (int kt = 0; kt < KB; ++kt) {
+        const int cur = (kt & 1) * STAGE, nxt = STAGE - cur;
+        float s_new[MT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const int8v w = operand(Wt + j * 16 * KB8);
+            if (j == NT - 1) {
+                // every load of step kt + 1 has landed and every read of step kt is done
+                __builtin_amdgcn_s_waitcnt(0);
+                debug_stage_sync();
+                __syncthreads();
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    const float next = sa[t] * sb;
+                    four[t] = (kt & 3) == 3 ? next : four[t];
+                    s_new[t] = of_step(four[t], kt + 1);
+                }
+                load_scales((kt >> 2) + 1, (kt & 3) == 2);
+                w[0] = operand(nxt + w_base);      // (stale data after the last step, unused)
+            } else {
+                w[(j + 1) & 1] = operand(cur + w_base + (j + 1) * 16 * KB8);
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                const float4v p = mfma_fp8(w, a[i], float4v{0.f, 0.f, 0.f, 0.f});
+                const int t = j * MT + i, u = t - 2;      // this tile, the tile folded now
+                p[t & 3] = mfma_fp8(w[j & 1], a[i], float4v{0.f, 0.f, 0.f, 0.f});
+                const int ui = u < 0 ? (u + MT * NT) % MT : u % MT, uj = u < 0 ? (u + MT * NT) / MT : u / MT;
+                const float us = u < 0 ? s_old[ui] : s[ui];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], s[i], acc[i][j][r]);
+                for (int r = 0; r < 4; ++r) acc[ui][uj][r] = __builtin_fmaf(p[u & 3][r], us, acc[ui][uj][r]);
+                const int slot = j == NT - 1 ? i : (j + 1) * MT + i;
+                if (slot % GAP == 0 && slot / GAP < PIECES) load_piece(j == NT - 1 ? kt + 2 : kt + 1, slot / GAP);
+                if (j == NT - 1) a[i] = operand(nxt + a_base + i * 16 * KB8);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            s_old[t] = s[t];
+            s[t] = s_new[t];
+        }
     }
+#pragma unroll
+    for (int u = MT * NT - 2; u < MT * NT; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            acc[u % MT][u / MT][r] = __builtin_fmaf(p[u & 3][r], s_old[u % MT], acc[u % MT][u / MT][r]);
 
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));     // the last (empty) loads to LDS
     const bool wide = N % 4 == 0 && ((uintptr_t)C & 7) == 0;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -212,19 +349,173 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const int n = n0 + (wn * NT + j) * 16 + 4 * (lane >> 4);
-            uint16_t h[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) h[r] = bad[i] ? 0 : out16<BF16>(acc[i][j][r]);
-            uint16_t *c = C + (size_t)m * N + n;
-            if (wide) {
-                if (n < N)
-                    *reinterpret_cast<uint2v *>(c) = uint2v{h[0] | (unsigned)h[1] << 16, h[2] | (unsigned)h[3] << 16};
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (n + r < N) c[r] = h[r];
-            }
+            store4<BF16>(C + (size_t)m * N + n, acc[i][j], bad[i], n, N, wide);
         }
+    }
+}
+
+// ---- streaming kernel, few rows ----
+// For row blocks of 16 MT <= 64 rows the weights are read once.  A workgroup
+// holds NT 16-column tiles; its NW waves take the 128-k steps in turn, each with
+// a ring of P stages in LDS of its own, so that nothing waits for another wave
+// until the partial sums meet, in the order of the waves.  Every load of a
+// stage (W tile, A tile, the rows' scales and the weight block's) goes straight
+// to LDS: eight lanes read one 128-byte line (loads to the operand registers
+// reach 64 bytes of a row at a time and stream at half the rate), and the
+// wave's counted wait is exact because it has no other loads.
+template <int N>
+__device__ inline void wait_loads()
+{
+    // (a compiler barrier too: the stage's LDS reads stay behind it)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <int MT, int NT, int NW, int P, bool BF16>
+__global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(
+    const uint8_t *__restrict__ Aall, const float *__restrict__ a_scale,
+    const int32_t *__restrict__ a_rows, int M_a, const uint8_t *__restrict__ Wall,
+    const float *__restrict__ Sall, const int32_t *__restrict__ offsets, int E, int M, int N,
+    int K, int KB, int NB, uint16_t *__restrict__ C)
+{
+    constexpr int BM = 16 * MT, BN = 16 * NT;
+    constexpr int LW = BN / 8, LA = BM / 8, L = LW + LA + 2;     // loads of a stage
+    constexpr int STAGE = (BN + BM) * KB8 + 512;                 // tiles, then 64 row scales, then the weight's
+    static_assert(MT <= 4 && 128 % BN == 0, "one load for the rows' scales, one weight scale");
+    static_assert((P - 1) * L < 64, "vmcnt holds 6 bits");
+    static_assert(MT * NT * 1024 <= P * STAGE, "the partial sums fit in the ring");
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int nbn = (N + BN - 1) / BN;
+    const int rb = blockIdx.x / nbn, n0 = (blockIdx.x - rb * nbn) * BN;
+    const RowBlock blk = find_rows(offsets, E, M, BM, rb);
+    const int e = __builtin_amdgcn_readfirstlane(blk.e);
+    const int m0 = __builtin_amdgcn_readfirstlane(blk.m0);
+    const int m1 = __builtin_amdgcn_readfirstlane(blk.m1);
+    if (m0 >= m1) return;      // no such row block: uniform, before the barrier
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, q = lane >> 4;
+    const int rows_n = N - n0 < BN ? N - n0 : BN;
+    const __amdgpu_buffer_rsrc_t w_rs = buffer_rsrc(Wall + ((size_t)e * N + n0) * K, (size_t)rows_n * K);
+    const __amdgpu_buffer_rsrc_t a_rs =
+        a_rows ? buffer_rsrc(Aall, (size_t)M_a * K) : buffer_rsrc(Aall + (size_t)m0 * K, (size_t)(m1 - m0) * K);
+    const __amdgpu_buffer_rsrc_t sa_rs = a_rows ? buffer_rsrc(a_scale, (size_t)M_a * KB * 4)
+                                                : buffer_rsrc(a_scale + (size_t)m0 * KB, (size_t)(m1 - m0) * KB * 4);
+    const __amdgpu_buffer_rsrc_t sw_rs = buffer_rsrc(Sall + ((size_t)e * NB + n0 / 128) * KB, (size_t)KB * 4);
+
+    // row of A that row i of the block takes (the last row again past the end),
+    // -1 for an index that names none
+    auto row_of = [&](int i) {
+        i = m0 + i < m1 ? i : m1 - 1 - m0;
+        if (!a_rows) return i;
+        const int r = a_rows[m0 + i];
+        return (unsigned)r < (unsigned)M_a ? r : -1;
+    };
+    const int chunk = (lane & 7) ^ (lane >> 3);
+    unsigned w_off[LW], a_off[LA];
+#pragma unroll
+    for (int i = 0; i < LW; ++i) {
+        int r = i * 8 + (lane >> 3);
+        r = r < rows_n ? r : rows_n - 1;
+        w_off[i] = (unsigned)r * (unsigned)K + chunk * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+        const int r = row_of(i * 8 + (lane >> 3));
+        a_off[i] = (unsigned)(r < 0 ? 0 : r) * (unsigned)K + chunk * 16;
+    }
+    const int srow = row_of(lane < BM ? lane : 0);
+    const unsigned s_off = (unsigned)(srow < 0 ? 0 : srow) * (unsigned)KB * 4u;
+    uint8_t *ring = lds + wave * (P * STAGE);
+
+    // (chunks past the end of K, and steps past the last, read nothing and give
+    // zeros, scales too)
+    auto load = [&](int kt, int sl) {
+        uint8_t *base = ring + sl * STAGE;
+        const bool in = kt * KB8 + chunk * 16 < K;
+#pragma unroll
+        for (int i = 0; i < LW; ++i) {
+            unsigned off = in ? w_off[i] : FP8_PAST;
+            pin(off);
+            uint8_t *dst = base + i * 1024;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rs, (__attribute__((address_space(3))) void *)dst, 16, off, kt * KB8, 0, QG_NT);
+        }
+#pragma unroll
+        for (int i = 0; i < LA; ++i) {
+            unsigned off = in ? a_off[i] : FP8_PAST;
+            pin(off);
+            uint8_t *dst = base + (LW + i) * 1024;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rs, (__attribute__((address_space(3))) void *)dst, 16, off, kt * KB8, 0, 0);
+        }
+        unsigned os = kt < KB ? s_off : FP8_PAST, ow = kt < KB ? 0u : FP8_PAST;
+        pin(os);
+        pin(ow);
+        uint8_t *dst = base + (LW + LA) * 1024;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(sa_rs, (__attribute__((address_space(3))) void *)dst, 4, os, kt * 4, 0, 0);
+        dst += 256;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(sw_rs, (__attribute__((address_space(3))) void *)dst, 4, ow, kt * 4, 0, 0);
+    };
+
+    float4v acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
+    const int o0 = c * KB8 + ((q ^ (lane & 7)) * 16);
+#pragma unroll
+    for (int i = 0; i < P; ++i) load(wave + i * NW, i);
+    for (int kt = wave; kt < KB; kt += P * NW) {
+#pragma unroll
+        for (int sl = 0; sl < P; ++sl) {
+            // the oldest stage has landed: at most the P - 1 younger ones' loads are in flight
+            if (QG_DEBUG_SYNC) wait_loads<0>();
+            else wait_loads<(P - 1) * L>();
+            const uint8_t *base = ring + sl * STAGE;
+            auto operand = [&](int tile) {
+                const int4v lo = *reinterpret_cast<const int4v *>(base + tile * 16 * KB8 + o0);
+                const int4v hi = *reinterpret_cast<const int4v *>(base + tile * 16 * KB8 + (o0 ^ 64));
+                return int8v{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            };
+            const float *sc = reinterpret_cast<const float *>(base + (LW + LA) * 1024);
+            int8v a[MT], w[NT];
+            float s[MT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) w[j] = operand(j);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                a[i] = operand(NT + i);
+                s[i] = sc[16 * i + c] * sc[64 + lane];
+            }
+            // the stage is in registers: refill it
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            load(kt + (sl + P) * NW, sl);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const float4v p = mfma_fp8(w[j], a[i], float4v{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], s[i], acc[i][j][r]);
+                }
+        }
+    }
+    // the last (empty) loads would write over the partial sums
+    wait_loads<0>();
+    float4v *part = reinterpret_cast<float4v *>(ring);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) part[(i * NT + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    const bool wide = N % 4 == 0 && ((uintptr_t)C & 7) == 0;
+#pragma unroll
+    for (int t = 0; t < MT * NT; ++t) {
+        if (t % NW != wave) continue;
+        const int i = (t / NT) * 16 + c, n = n0 + (t % NT) * 16 + 4 * q;
+        float4v x = *(reinterpret_cast<const float4v *>(lds) + t * 64 + lane);
+#pragma unroll
+        for (int w = 1; w < NW; ++w)
+            x += *(reinterpret_cast<const float4v *>(lds + w * (P * STAGE)) + t * 64 + lane);
+        if (m0 + i < m1) store4<BF16>(C + (size_t)(m0 + i) * N + n, x, row_of(i) < 0, n, N, wide);
     }
 }
 
@@ -242,10 +533,55 @@ struct Fp8Args {
 
 // Upper bound on the BM-row blocks of M rows in E experts: every non-empty
 // expert may end in a partial block.
-long long row_blocks(const Fp8Args &a, int BM)
+long long row_blocks(bool grouped, int E, int M, int BM)
 {
-    if (!a.offsets) return (a.M + BM - 1) / BM;
-    return (long long)a.M / BM + (a.E < a.M ? a.E : a.M);
+    if (!grouped) return (M + BM - 1) / BM;
+    return (long long)M / BM + (E < M ? E : M);
+}
+
+// The kernel of a call: the streaming ones by their m-tiles, n-tiles and waves,
+// the tiled ones by their tile.
+enum Fp8Kernel { S1x2x4, S1x2x2, S1x1x4, S2x2x4, S2x4x2, S4x2x4, S4x4x4, T64x128, T256x256 };
+
+struct Fp8Shape {
+    const char *name;
+    int bm, bn, threads;
+};
+constexpr Fp8Shape FP8_SHAPES[] = {
+    {"streaming, 16 x 32, 4 waves over k", 16, 32, 256},  {"streaming, 16 x 32, 2 waves over k", 16, 32, 128},
+    {"streaming, 16 x 16, 4 waves over k", 16, 16, 256},  {"streaming, 32 x 32, 4 waves over k", 32, 32, 256},
+    {"streaming, 32 x 64, 2 waves over k", 32, 64, 128},  {"streaming, 64 x 32, 4 waves over k", 64, 32, 256},
+    {"streaming, 64 x 64, 4 waves over k", 64, 64, 256},  {"tiled, 64 x 128", 64, 128, 256},
+    {"tiled, 256 x 256", 256, 256, 512}};
+
+// By the rows an expert has on average (the host does not know the counts; an
+// uneven split is slower, never wrong) and the workgroups that makes.  Both
+// sides measured in us at K x N = 5120 x 17408 unless stated.
+Fp8Kernel choose(bool grouped, int E, int M, int N, int K)
+{
+    const long long active = grouped ? (E < M ? E : M) : 1;
+    const long long rows = (M + active - 1) / active;
+    auto wgs = [&](int bm, int bn) { return active * ((rows + bm - 1) / bm) * ((N + bn - 1) / bn); };
+    if (rows <= 16) {
+        // enough workgroups that a smaller share of K each pays: 16 tokens to 8 of
+        // 64 experts at 2048 x 7168: 114 (two waves) against 129 (four)
+        if (wgs(16, 32) >= 2048) return S1x2x2;
+        // too few for the chip and a short K: four rows at 2048 x 2048: 3.9
+        // (16 columns) against 4.4 (32); at 17408 x 5120 28.5 against 22.5
+        if (wgs(16, 32) < 128 && K <= 4096) return S1x1x4;
+        return S1x2x4;                                   // one row: 18.8, tiled 43.9
+    }
+    // 32 rows: 27.2, as two blocks of 16 35.0, tiled 44.4; 16 rows an
+    // expert in 64 experts at 2048 x 7168: 174 (32 x 64) against 225 (32 x 32)
+    if (rows <= 32) return wgs(32, 32) >= 2048 ? S2x4x2 : S2x2x4;
+    // 64 rows: 39.7 (64 columns), 42.7 (32 columns), tiled 45.3; at 17408 x 5120
+    // 56.7, 42.9 and 134.  Many experts fill the chip without the split over k: 32
+    // rows an expert in 64 experts at 2048 x 7168: 197 tiled, 228 streaming
+    if (rows <= 64 && wgs(64, 128) < 1024) return wgs(64, 64) >= 256 ? S4x4x4 : S4x2x4;
+    // 512 rows (136 tiles of 256 x 256): 88 against 103 for 64 x 128; 256 rows (68
+    // tiles): 89 against 67; 512 rows at 17408 x 5120 (40 tiles): 249 against 142
+    if (rows > 128 && wgs(256, 256) >= 128) return T256x256;
+    return T64x128;
 }
 
 template <int BM, int BN, int WM, int WN, bool BF16>
@@ -257,16 +593,42 @@ hipError_t tiled(const Fp8Args &a, hipStream_t st)
         const hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    const long long wgs = row_blocks(a, BM) * ((a.N + BN - 1) / BN);
+    const long long wgs = row_blocks(a.offsets != nullptr, a.E, a.M, BM) * ((a.N + BN - 1) / BN);
     hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(64 * WM * WN), bytes, st, a.A, a.a_scale, a.a_rows,
                        a.M_a, a.W, a.w_scale, a.offsets, a.E, a.M, a.N, a.K, a.KB, a.NB, a.C);
+    return hipGetLastError();
+}
+
+template <int MT, int NT, int NW, int P, bool BF16>
+hipError_t stream(const Fp8Args &a, hipStream_t st)
+{
+    const auto kern = fp8_stream_kernel<MT, NT, NW, P, BF16>;
+    constexpr int bytes = NW * P * (16 * (MT + NT) * KB8 + 512);
+    if (bytes > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+    }
+    const long long wgs = row_blocks(a.offsets != nullptr, a.E, a.M, 16 * MT) * ((a.N + 16 * NT - 1) / (16 * NT));
+    hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(64 * NW), bytes, st, a.A, a.a_scale, a.a_rows, a.M_a, a.W,
+                       a.w_scale, a.offsets, a.E, a.M, a.N, a.K, a.KB, a.NB, a.C);
     return hipGetLastError();
 }
 
 template <bool BF16>
 hipError_t launch(const Fp8Args &a, hipStream_t st)
 {
-    return tiled<64, 128, 2, 2, BF16>(a, st);
+    switch (choose(a.offsets != nullptr, a.E, a.M, a.N, a.K)) {
+    case S1x2x4: return stream<1, 2, 4, 2, BF16>(a, st);
+    case S1x2x2: return stream<1, 2, 2, 2, BF16>(a, st);
+    case S1x1x4: return stream<1, 1, 4, 2, BF16>(a, st);
+    case S2x2x4: return stream<2, 2, 4, 2, BF16>(a, st);
+    case S2x4x2: return stream<2, 4, 2, 2, BF16>(a, st);
+    case S4x2x4: return stream<4, 2, 4, 2, BF16>(a, st);
+    case S4x4x4: return stream<4, 4, 4, 2, BF16>(a, st);
+    case T64x128: return tiled<64, 128, 2, 2, BF16>(a, st);
+    case T256x256: return tiled<256, 256, 4, 2, BF16>(a, st);
+    }
+    return hipErrorUnknown;
 }
 
 } // namespace
@@ -280,18 +642,15 @@ hipError_t launch_fp8(const uint8_t *A, const float *a_scale, const int32_t *a_r
     return dtype == QG_DT_BF16 ? launch<true>(a, st) : launch<false>(a, st);
 }
 
-long long fp8_workgroups(bool grouped, int E, int M, int N, int K)
+long long fp8_threads(bool grouped, int E, int M, int N, int K)
 {
-    Fp8Args a = {};
-    a.offsets = grouped ? (const int32_t *)1 : nullptr;
-    a.E = E;
-    a.M = M;
-    return row_blocks(a, 64) * ((N + 127) / 128);
+    const Fp8Shape &k = FP8_SHAPES[choose(grouped, E, M, N, K)];
+    return row_blocks(grouped, E, M, k.bm) * ((N + k.bn - 1) / k.bn) * k.threads;
 }
 
 void describe_fp8(bool grouped, int E, int M, int N, int K, char *buf, size_t n)
 {
-    snprintf(buf, n, "tiled kernel, 64 x 128");
+    snprintf(buf, n, "%s", FP8_SHAPES[choose(grouped, E, M, N, K)].name);
 }
 
 } // namespace qg

@@ -154,8 +154,8 @@ hipError_t launch_quantize_rows_fp8(const void *A, int dtype, int M, int K, bool
 hipError_t launch_fp8(const uint8_t *A, const float *a_scale, const int32_t *a_rows, int M_a,
                       const uint8_t *W, const float *w_scale, const int32_t *offsets, int E, int M,
                       int N, int K, int dtype, void *C, hipStream_t st);
-// Workgroups of the launch (the caller refuses what exceeds a grid).
-long long fp8_workgroups(bool grouped, int E, int M, int N, int K);
+// Threads of the launch (the caller refuses what exceeds a grid).
+long long fp8_threads(bool grouped, int E, int M, int N, int K);
 void describe_fp8(bool grouped, int E, int M, int N, int K, char *buf, size_t n);
 
 // flags: QG_ROUTE_* of the C ABI.

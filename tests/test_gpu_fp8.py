@@ -174,6 +174,32 @@ def test_dense(M, N, K, dtype):
     check(C, *dequant(a, sa, w, sw), dtype)
 
 
+# one shape or two of every kernel the rule on rows and workgroups can choose that
+# the small shapes above do not reach (its thresholds: 16, 32, 64 and 128 rows,
+# 128, 256, 1024 and 2048 workgroups, K 4096)
+@pytest.mark.parametrize("M,N,K", [
+    (3, 65540, 272), (16, 65600, 4112), (9, 4100, 4112), (16, 4096, 1040), (20, 65600, 272), (32, 70000, 144),
+    (40, 16400, 272), (64, 16384, 1168), (50, 8200, 4112), (300, 16500, 400), (512, 17408, 5120), (1025, 8196, 656)])
+def test_dense_wide(M, N, K):
+    note(f"fp8_gemm M={M} N={N} K={K}")
+    a, w = codes((M, K), 1), codes((N, K), 2)
+    sa, sw = scales((M, kb(K)), 3), scales((kb(N), kb(K)), 4)
+    C = torch.full((M, N), float("nan"), dtype=torch.float16, device="cuda")
+    qg.fp8_gemm(a, sa, w, sw, C=C)
+    torch.cuda.synchronize()
+    # every column block's edge and a stretch of each, to keep the 64-bit product small
+    cols = torch.cat([torch.arange(0, 260), torch.arange(N // 2, N // 2 + 130), torch.arange(N - 261, N)])
+    part = (cols // 128).cuda()
+    cols = cols.cuda()
+    assert bool(C.isfinite().all())
+    A = a.double() * sa.double().repeat_interleave(128, 1)[:, :K]
+    fw = sw[part].double().repeat_interleave(128, 1)[:, :K]
+    wv, av = w[cols].double(), a.double()
+    up = lambda v: torch.where(v != 0, v.abs().clamp_min(2.0**-6), 0.0)
+    fa = sa.double().repeat_interleave(128, 1)[:, :K]
+    check(C[:, cols], A.cpu(), (wv * fw).cpu(), (up(av) * fa).float(), (up(wv) * fw).float(), torch.float16)
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 130, 272), (70, 260, 640), (300, 384, 1152)])
 def test_exact_on_small_integers(M, N, K):
     """Codes -4..4 and power-of-two scales: every sum is exact, so is C."""
@@ -202,6 +228,10 @@ GROUPED = [
     ([300, 0, 257, 1], 132, 400, 128, 0, 1),
     ([0, 0, 0], 64, 128, 4, 0, 6),
     ([129, 128, 127, 200, 90, 333], 516, 512, 700, 0, 0),
+    # the same, large enough for the large tile and the streaming kernels of many workgroups
+    ([129, 0, 700, 200, 90, 333], 8200, 272, 700, 3, 2),
+    ([1, 2, 3, 0, 16, 17, 5, 9], 16400, 272, 40, 0, 1),
+    ([30, 20, 31, 0, 70, 17, 5, 9], 16400, 144, 40, 0, 1),
 ]
 
 
