@@ -419,27 +419,36 @@ def _dtype(t: torch.Tensor, name: str, f32=False) -> int:
 
 
 def _arg(t: Optional[torch.Tensor], dtype, shape, device, name):
-    """A device tensor of this type, shape and device, contiguous; its pointer."""
+    """The pointer of a contiguous device tensor of this type, shape and device."""
     if t is None:
         return None
-    p = _ptr(t, dtype, name)
+    if (isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype is dtype) and t.shape == shape and
+            t.device == device and t.is_contiguous()):
+        return t.data_ptr()
+    _ptr(t, dtype, name)         # says what is wrong, if it is one of its checks
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return p
+    raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _raw_stream(index: int) -> int:
+    """The handle of a device's current stream, without a Stream object where
+    torch offers that (1.8 us less of a 7 us call)."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def _call(fn, device, *args):
     """fn(*args, stream) on `device`'s current stream; the library launches on
     the current device, so another one is made current for the call."""
-    st = torch.cuda.current_stream(device).cuda_stream
+    st = _raw_stream(device.index)
     if device.index == torch.cuda.current_device():
         rc = fn(*args, st)
     else:
         with torch.cuda.device(device):
             rc = fn(*args, st)
-    _check(rc)
+    if rc != QG_OK:
+        _check(rc)
 
 
 def _blocks128(n: int) -> int:
