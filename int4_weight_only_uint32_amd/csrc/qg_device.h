@@ -154,6 +154,26 @@ __device__ inline float silu_mul(float g, float u)
     return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
+// exp(x) for -150 <= x <= 88 within 2^-22 of its value: the hardware's 2^t (one
+// step of 2^-23) on t = x log2(e) rounded, times 1 + r ln 2 for the part r that
+// the rounding lost.
+__device__ inline float exp_near(float x)
+{
+    constexpr float L2E = 0x1.715476p+0f, L2E_LO = 0x1.4ae0c0p-26f, LN2 = 0x1.62e430p-1f;
+    const float t = x * L2E;
+    const float r = __builtin_fmaf(x, L2E_LO, __builtin_fmaf(x, L2E, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(e * LN2, r, e);
+}
+
+// 1 / d for 1 <= d < 2^127, within one step: the hardware's reciprocal and a
+// Newton step.
+__device__ inline float rcp_near(float d)
+{
+    const float y = __builtin_amdgcn_rcpf(d);
+    return __builtin_fmaf(__builtin_fmaf(-d, y, 1.0f), y, y);
+}
+
 // Gate/up pairs in the GEMM kernels (GATED): the pair is one packed [K, 2Nh]
 // weight, gate columns first.  A kernel runs over the pair's 2Nh columns in a
 // virtual order that interleaves the two halves by 16-column tile -- virtual

@@ -76,26 +76,6 @@ __device__ inline float key_value(unsigned k)
     return __builtin_bit_cast(float, k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// exp(x) for -150 <= x <= 88 within 2^-22 of its value: the hardware's 2^t (one
-// step of 2^-23) on t = x log2(e) rounded, times 1 + r ln 2 for the part r that
-// the rounding lost.
-__device__ inline float exp_near(float x)
-{
-    constexpr float L2E = 0x1.715476p+0f, L2E_LO = 0x1.4ae0c0p-26f, LN2 = 0x1.62e430p-1f;
-    const float t = x * L2E;
-    const float r = __builtin_fmaf(x, L2E_LO, __builtin_fmaf(x, L2E, -t));
-    const float e = __builtin_amdgcn_exp2f(t);
-    return __builtin_fmaf(e * LN2, r, e);
-}
-
-// 1 / d for 1 <= d < 2^127, within one step: the hardware's reciprocal and a
-// Newton step.
-__device__ inline float rcp_near(float d)
-{
-    const float y = __builtin_amdgcn_rcpf(d);
-    return __builtin_fmaf(__builtin_fmaf(-d, y, 1.0f), y, y);
-}
-
 __device__ inline float sigmoid_near(float l)
 {
     // (clamped: below, the result is under 2^-126 and the caller's sums tell)
