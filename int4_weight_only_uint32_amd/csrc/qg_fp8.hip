@@ -130,7 +130,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     const uint8_t *__restrict__ Aall, const float *__restrict__ a_scale,
     const int32_t *__restrict__ a_rows, int M_a, const uint8_t *__restrict__ Wall,
     const float *__restrict__ Sall, const int32_t *__restrict__ offsets, int E, int M, int N,
-    int K, int KB, int NB, uint16_t *__restrict__ C)
+    int K, int KB, int NB, int col_first, int nbn, uint16_t *__restrict__ C)
 {
     constexpr int NW = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
     constexpr int LA = BM / 8 / NW, LW = BN / 8 / NW;    // 1 KB loads per wave and step
@@ -139,11 +139,10 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr int STAGE = (BM + BN) * KB8;
 
-    const int nbn = (N + BN - 1) / BN;
     int rb, n0;
     // uniform over the workgroup, before any barrier
     if (!tile_of<1024 / BM>(blockIdx.x, row_block_count(offsets, E, M, BM), nbn, rb, n0)) return;
-    n0 *= BN;
+    n0 = col_first + n0 * BN;
     const RowBlock blk = find_rows(offsets, E, M, BM, rb);
     const int e = __builtin_amdgcn_readfirstlane(blk.e);
     const int m0 = __builtin_amdgcn_readfirstlane(blk.m0);
@@ -250,15 +249,11 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     float4v p[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) p[t] = float4v{0.f, 0.f, 0.f, 0.f};
-    // (no branch: where `now` is false the loads read nothing)
-    auto load_scales = [&](int c, bool now) {
-        unsigned off = now ? (unsigned)(lane >> 4) * 4u : FP8_PAST;
-        pin(off);
-        sb = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sw_rs, off, c * 16, 0));
+    auto load_scales = [&](int c) {
+        sb = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sw_rs, (lane >> 4) * 4, c * 16, 0));
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            unsigned o = now ? s_off[t] : FP8_PAST;
-            pin(o);
+            const unsigned o = s_off[t];
             sa[t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sa_rs, o, c * 16, 0));
         }
     };
@@ -266,7 +261,27 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
         const int from = ((kt & 3) * 16 + (lane & 15)) * 4;
         return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, x)));
     };
-    load_scales(0, true);
+    if (m0 + wm * MT * 16 >= m1) {
+        // None of this wave's rows exist (the last block of an expert's rows): it
+        // keeps loading and meeting the others at the barriers, and leaves the
+        // matrix cores to them.
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) load_piece(0, q);
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) load_piece(1, q);
+        for (int kt = 0; kt < KB; ++kt) {
+            __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < PIECES; ++q) load_piece(kt + 2, q);
+        }
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+        __syncthreads();
+        return;
+    }
+    load_scales(0);
 #pragma unroll
     for (int q = 0; q < PIECES; ++q) load_piece(0, q);
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
@@ -277,23 +292,24 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
         s[t] = of_step(four[t], 0);
         s_old[t] = 0.f;
     }
-    // Loads are spread over the MFMAs of half a step, one after every GAP of
-    // them: a burst of all of them behind the barrier holds every wave's issue
-    // until the address unit has taken them.  Slot i of the last column tile and
-    // slot (j + 1) * MT + i of column tile j of the next step.
-    constexpr int GAP = NT / 2 * MT / PIECES > 0 ? NT / 2 * MT / PIECES : 1;
-    static_assert(GAP * PIECES <= NT * MT, "every load has a slot");
+    // Loads go out one behind each of the first MFMAs after the barrier: in one
+    // burst behind it they hold every wave's issue until the address unit has
+    // taken them (289 against 278 us at 4096 x 8192 x 8192), and further apart
+    // they land late (243 against 237).  Slot i is behind MFMA i of the last column
+    // tile, slot (j + 1) * MT + i behind MFMA i of column tile j of the next step.
+    static_assert(PIECES <= NT * MT, "every load has a slot");
 #pragma unroll
-    for (int i = 0; i < MT; i += GAP)
-        if (i / GAP < PIECES) load_piece(1, i / GAP);
+    for (int i = 0; i < MT; ++i)
+        if (i < PIECES) load_piece(1, i);
     int8v a[MT], w[2];
     w[0] = operand(w_base);
 #pragma unroll
     for (int i = 0; i < MT; ++i) a[i] = operand(a_base + i * 16 * KB8);
     static_assert(NT % 2 == 0 && MT * NT % 4 == 0, "rings of two operands and four products");
 
-    for (int kt = 0; kt < KB; ++kt) {
-        const int cur = (kt & 1) * STAGE, nxt = STAGE - cur;
+    // one step; at = kt % 4, a constant at each call
+    auto step = [&](int kt, int at) __attribute__((always_inline)) {
+        const int cur = (at & 1) * STAGE, nxt = STAGE - cur;
         float s_new[MT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -304,11 +320,10 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
                 __syncthreads();
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
-                    const float next = sa[t] * sb;
-                    four[t] = (kt & 3) == 3 ? next : four[t];
-                    s_new[t] = of_step(four[t], kt + 1);
+                    if (at == 3) four[t] = sa[t] * sb;
+                    s_new[t] = of_step(four[t], at + 1);
                 }
-                load_scales((kt >> 2) + 1, (kt & 3) == 2);
+                if (at == 2) load_scales((kt >> 2) + 1);
                 w[0] = operand(nxt + w_base);      // (stale data after the last step, unused)
             } else {
                 w[(j + 1) & 1] = operand(cur + w_base + (j + 1) * 16 * KB8);
@@ -323,7 +338,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[ui][uj][r] = __builtin_fmaf(p[u & 3][r], us, acc[ui][uj][r]);
                 const int slot = j == NT - 1 ? i : (j + 1) * MT + i;
-                if (slot % GAP == 0 && slot / GAP < PIECES) load_piece(j == NT - 1 ? kt + 2 : kt + 1, slot / GAP);
+                if (slot < PIECES) load_piece(j == NT - 1 ? kt + 2 : kt + 1, slot);
                 if (j == NT - 1) a[i] = operand(nxt + a_base + i * 16 * KB8);
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -333,6 +348,19 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
             s_old[t] = s[t];
             s[t] = s_new[t];
         }
+    };
+    // (four steps to a round, for the scales; no branch inside a step: the
+    // compiler would sink the FMAs before it to where it joins again, and keep
+    // all products alive)
+    for (int kt = 0;; kt += 4) {
+        step(kt, 0);
+        if (kt + 1 >= KB) break;
+        step(kt + 1, 1);
+        if (kt + 2 >= KB) break;
+        step(kt + 2, 2);
+        if (kt + 3 >= KB) break;
+        step(kt + 3, 3);
+        if (kt + 4 >= KB) break;
     }
 #pragma unroll
     for (int u = MT * NT - 2; u < MT * NT; ++u)
@@ -340,15 +368,49 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
         for (int r = 0; r < 4; ++r)
             acc[u % MT][u / MT][r] = __builtin_fmaf(p[u & 3][r], s_old[u % MT], acc[u % MT][u / MT][r]);
 
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));     // the last (empty) loads to LDS
+    // The tile goes out through LDS: a lane holds four columns of one row, so that
+    // storing from registers would write 32 bytes of a 128-byte line at a time.  Each
+    // wave lays its own rows out (chunk c of 16 bytes of row r at c ^ (r % 16),
+    // against bank conflicts) and writes them 16 bytes a lane.
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));     // the last (empty) loads to LDS, of every wave
+    __syncthreads();
+    constexpr int ROW = NT * 16 * 2, CH = ROW / 16, RPI = 64 / CH;   // bytes and chunks of a row, rows of one store
+    static_assert(MT * 16 * ROW * NW <= 2 * STAGE && CH >= 2 && CH <= 16, "the tile fits, a row in 16 chunks");
+    const int row0 = m0 + wm * MT * 16, col0 = n0 + wn * NT * 16;
+    if (N % 8 == 0 && ((uintptr_t)C & 15) == 0) {
+        uint8_t *mine = lds + wave * (MT * 16 * ROW);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                uint16_t h[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) h[r] = bad[i] ? 0 : out16<BF16>(acc[i][j][r]);
+                const int r = i * 16 + (lane & 15), c = j * 2 + (lane >> 5);
+                *reinterpret_cast<uint2v *>(mine + r * ROW + ((c ^ r) & (CH - 1)) * 16 + ((lane >> 4) & 1) * 8) =
+                    uint2v{h[0] | (unsigned)h[1] << 16, h[2] | (unsigned)h[3] << 16};
+            }
+        // (the wave reads back its own words, in order)
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+        for (int k = 0; k < MT * 16 / RPI; ++k) {
+            const int r = k * RPI + lane / CH, c = lane % CH;
+            const uint4v v = *reinterpret_cast<const uint4v *>(mine + r * ROW + ((c ^ r) & (CH - 1)) * 16);
+            if (row0 + r < m1 && col0 + c * 8 < N)
+                __builtin_nontemporal_store(v, reinterpret_cast<uint4v *>(C + (size_t)(row0 + r) * N + col0 + c * 8));
+        }
+        return;
+    }
     const bool wide = N % 4 == 0 && ((uintptr_t)C & 7) == 0;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-        const int m = m0 + (wm * MT + i) * 16 + (lane & 15);
+        const int m = row0 + i * 16 + (lane & 15);
         if (m >= m1) continue;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const int n = n0 + (wn * NT + j) * 16 + 4 * (lane >> 4);
+            const int n = col0 + j * 16 + 4 * (lane >> 4);
             store4<BF16>(C + (size_t)m * N + n, acc[i][j], bad[i], n, N, wide);
         }
     }
@@ -584,8 +646,9 @@ Fp8Kernel choose(bool grouped, int E, int M, int N, int K)
     return T64x128;
 }
 
+// The tiled kernel on columns col_first .. col_end - 1 (col_first a multiple of 128).
 template <int BM, int BN, int WM, int WN, bool BF16>
-hipError_t tiled(const Fp8Args &a, hipStream_t st)
+hipError_t tiled(const Fp8Args &a, int col_first, int col_end, hipStream_t st)
 {
     const auto kern = fp8_tiled_kernel<BM, BN, WM, WN, BF16>;
     constexpr int bytes = 2 * (BM + BN) * KB8;
@@ -593,10 +656,23 @@ hipError_t tiled(const Fp8Args &a, hipStream_t st)
         const hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    const long long wgs = row_blocks(a.offsets != nullptr, a.E, a.M, BM) * ((a.N + BN - 1) / BN);
+    const int nbn = (col_end - col_first + BN - 1) / BN;
+    const long long wgs = row_blocks(a.offsets != nullptr, a.E, a.M, BM) * nbn;
     hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(64 * WM * WN), bytes, st, a.A, a.a_scale, a.a_rows,
-                       a.M_a, a.W, a.w_scale, a.offsets, a.E, a.M, a.N, a.K, a.KB, a.NB, a.C);
+                       a.M_a, a.W, a.w_scale, a.offsets, a.E, a.M, a.N, a.K, a.KB, a.NB, col_first, nbn, a.C);
     return hipGetLastError();
+}
+
+// Column blocks of 256 for the large tile, the rest for the 128 x 128 one: whole
+// rounds of the chip's 256 CUs, where what is left over would be less than half
+// a round (4096 x 17408 x 5120: 4.25 rounds).  All of them where the counts are
+// not the host's.
+int large_cols(const Fp8Args &a)
+{
+    const int rbs = (a.M + 255) / 256, nbn = (a.N + 255) / 256;
+    const long long tiles = (long long)rbs * nbn, over = tiles % 256;
+    if (a.offsets || tiles < 256 || over == 0 || over > 112) return nbn;
+    return (int)((tiles - over) / rbs);
 }
 
 template <int MT, int NT, int NW, int P, bool BF16>
@@ -625,8 +701,13 @@ hipError_t launch(const Fp8Args &a, hipStream_t st)
     case S2x4x2: return stream<2, 4, 2, 2, BF16>(a, st);
     case S4x2x4: return stream<4, 2, 4, 2, BF16>(a, st);
     case S4x4x4: return stream<4, 4, 4, 2, BF16>(a, st);
-    case T64x128: return tiled<64, 128, 2, 2, BF16>(a, st);
-    case T256x256: return tiled<256, 256, 4, 2, BF16>(a, st);
+    case T64x128: return tiled<64, 128, 2, 2, BF16>(a, 0, a.N, st);
+    case T256x256: {
+        const int end = large_cols(a) * 256;
+        if (end >= a.N) return tiled<256, 256, 4, 2, BF16>(a, 0, a.N, st);
+        const hipError_t e = tiled<256, 256, 4, 2, BF16>(a, 0, end, st);
+        return e != hipSuccess ? e : tiled<128, 128, 2, 2, BF16>(a, end, a.N, st);
+    }
     }
     return hipErrorUnknown;
 }

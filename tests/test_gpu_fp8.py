@@ -179,7 +179,8 @@ def test_dense(M, N, K, dtype):
 # 128, 256, 1024 and 2048 workgroups, K 4096)
 @pytest.mark.parametrize("M,N,K", [
     (3, 65540, 272), (16, 65600, 4112), (9, 4100, 4112), (16, 4096, 1040), (20, 65600, 272), (32, 70000, 144),
-    (40, 16400, 272), (64, 16384, 1168), (50, 8200, 4112), (300, 16500, 400), (512, 17408, 5120), (1025, 8196, 656)])
+    (40, 16400, 272), (64, 16384, 1168), (50, 8200, 4112), (300, 16500, 400), (512, 17408, 5120), (1025, 8196, 656),
+    (1000, 17500, 272), (1024, 17408, 144)])        # columns left over from whole rounds of the large tile
 def test_dense_wide(M, N, K):
     note(f"fp8_gemm M={M} N={N} K={K}")
     a, w = codes((M, K), 1), codes((N, K), 2)
