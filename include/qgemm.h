@@ -316,15 +316,15 @@ int quantize_rows_int8(const uint16_t *A, int M, int K, int8_t *A_q, float *a_sc
  * A        [M,K] fp16 or bf16 (dtype QG_DTYPE_F16 / QG_DTYPE_BF16)
  *          activations, 16-byte aligned; K % 16 == 0 (else
  *          QG_ERR_UNSUPPORTED).  With QG_QUANT_SWIGLU a [M,2K] gate/up pair
- *          (gate columns first), and x below is silu(gate) * up in binary32;
- *          without it x = A.
+ *          (gate columns first), and x below is silu(gate) * up, in 64 bits
+ *          wherever that decides a scale or a code; without it x = A.
  * A_q      [M,K] e4m3 codes out (OCP: largest value 448, no infinity),
  *          16-byte aligned; a_scale [M, ceil(K/128)] fp32 out.  For each row
  *          m and block b of 128 columns (the last may be partial):
  *            a_scale[m,b] = max |x| / 448
  *            A_q[m,k]     = e4m3(clamp(x[m,k] / a_scale[m,b], -448, 448))
- *          both quotients single IEEE binary32 operations, the code rounded
- *          to the nearest (ties to even).  A block of zeros gets scale 0 and
+ *          both quotients rounded once to binary32, the code rounded to the
+ *          nearest (ties to even).  A block of zeros gets scale 0 and
  *          codes 0; a block with a NaN or an infinity gets a NaN scale and
  *          NaN codes, so every product with it is NaN.
  * M == 0 is a call that does nothing.  One kernel on `stream`, no workspace. */

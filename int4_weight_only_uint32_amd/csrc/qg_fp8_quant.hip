@@ -9,15 +9,17 @@
 // rows of a 2 x 17408 bf16 pair (360 MB), 2.3, 3.1 and 5.0 on 16 x 5120.
 //
 // The code of x at scale sc is that of the correctly rounded quotient x / sc.
-// The division is costly (ten instructions a value: at 4096 rows of a
-// 2 x 17408 pair the kernel took 97 us with it), so the code is first taken
-// from y = x * inv, inv = 1 / sc correctly rounded: y is at most 2 steps of
-// binary32 from x / sc (two roundings of relative size 2^-24), the rounded
-// quotient half a step, so both are on the same side of every border between
-// two codes unless y is within 3 steps of one.  Borders of normal codes have
-// binary32's low 20 fraction bits equal to 0x80000.  Only next to them, below
-// 2^-6 (the codes' subnormals) and for scales whose inverse could overflow is
-// the division done.
+// The division is costly (ten instructions a value), so the code is first taken
+// from y = x * inv, inv = 1 / sc correctly rounded, twice: of y a little
+// smaller and a little larger, by more than y and the rounded quotient can
+// differ.  Equal codes are the quotient's too (rounding is monotone); only where
+// they are not, next to a border between two codes, is the division done.
+//
+// silu(gate) * up is formed in binary32 and is some steps off, which alone would
+// move a few codes and most scales by a step.  The same two codes tell where a
+// step could matter, and there the value is formed again in 64 bits; so is
+// the block's largest value, for the scale.  Codes and scales are then those of
+// the product in 64 bits.
 #include "qg_device.h"
 #include "qg_launch.h"
 
@@ -41,13 +43,25 @@ __device__ inline void widen8(const uint4v &a, float (&x)[8])
     }
 }
 
-// silu(g) * u in binary32, a few steps off.  Below -88 silu is 0 to 2e-37 |g|;
-// infinities and NaN give a NaN or an infinity.
+// silu(g) * u in binary32, within 2^-21 of its size.  Below -88 silu is 0 to
+// 2e-37 |g|; infinities and NaN give a NaN or an infinity.
 __device__ inline float silu_near(float g, float u)
 {
     const float x = __builtin_fminf(__builtin_fmaxf(-g, -87.0f), 88.0f);
     const float s = rcp_near(1.0f + exp_near(x));
     return g * (g > -88.0f ? s : 0.0f) * u;
+}
+
+__device__ inline double silu_64(float g, float u)
+{
+    return (double)g / (1.0 + exp(-(double)g)) * (double)u;
+}
+
+// Four e4m3 codes (nearest, ties to even; up to 464 gives 448, a NaN a NaN).
+__device__ inline unsigned code4(float a, float b, float c, float d)
+{
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (unsigned)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
 template <bool BF16, bool SWIGLU>
@@ -81,42 +95,73 @@ __global__ __launch_bounds__(256) void quantize_rows_fp8_kernel(
     for (int j = 0; j < 8; ++j)
         mx = __builtin_elementwise_max(mx, __builtin_bit_cast(unsigned, x[j]) & 0x7fffffffu);
     // over the 16 lanes of a block, by rotations of a row of 16
-#define QG_DPP_MAX(ctrl) \
-    mx = __builtin_elementwise_max(mx, (unsigned)__builtin_amdgcn_update_dpp(0, (int)mx, ctrl, 0xf, 0xf, false))
-    QG_DPP_MAX(0x128);
-    QG_DPP_MAX(0x124);
-    QG_DPP_MAX(0x122);
-    QG_DPP_MAX(0x121);
-#undef QG_DPP_MAX
-    float sc = __builtin_bit_cast(float, mx) / 448.0f;
-    if (mx >= 0x7f800000u) sc = __builtin_nanf("");
+#define QG_ROT_MAX(v, ctrl) \
+    v = __builtin_elementwise_max(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xf, 0xf, false))
+#define QG_ROW_MAX(v) QG_ROT_MAX(v, 0x128); QG_ROT_MAX(v, 0x124); QG_ROT_MAX(v, 0x122); QG_ROT_MAX(v, 0x121)
+    QG_ROW_MAX(mx);
+    float sc;
+    if (mx >= 0x7f800000u) {
+        sc = __builtin_nanf("");
+    } else if (SWIGLU) {
+        // the values that may be the largest: those within 2^-19 of it
+        const float near = __builtin_bit_cast(float, mx) * (1.0f - 0x1p-19f);
+        unsigned cand = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cand |= (__builtin_fabsf(x[j]) >= near && mx ? 1u : 0u) << j;
+        unsigned best = 0;
+        while (cand) {       // (one lane of the 16, once, as a rule)
+            float gj = 0.f, uj = 0.f, xg[8];
+            widen8<BF16>(g, xg);
+            const int at_j = __builtin_ctz(cand);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                gj = j == at_j ? xg[j] : gj;
+                uj = j == at_j ? y[j] : uj;
+            }
+            const float s = (float)(__builtin_fabs(silu_64(gj, uj)) / 448.0);
+            best = __builtin_elementwise_max(best, __builtin_bit_cast(unsigned, s));
+            cand &= cand - 1;
+        }
+        mx = mx ? best : 0u;
+        QG_ROW_MAX(mx);
+        sc = __builtin_bit_cast(float, mx);
+    } else {
+        sc = __builtin_bit_cast(float, mx) / 448.0f;
+    }
     if (sub == 0) a_scale[blk] = sc;
     if (!in) return;
-    const float inv = mx ? 1.0f / sc : 0.0f;
-    bool redo = sc < 0x1p-100f;
+    // y is off by 2 2^-24 (the inverse and the product), the rounded quotient by
+    // 2^-24, silu by up to 2^-21
+    constexpr float EPS = SWIGLU ? 0x1p-20f : 0x1p-21f;
+    const float inv = sc > 0.0f ? 1.0f / sc : sc;        // 0 for a block of zeros, NaN for a NaN
+    uint2v o, o2;
+    float t[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        y[j] = x[j] * inv;
-        const unsigned b = __builtin_bit_cast(unsigned, y[j]);
-        redo |= ((b - 0x7fffdu) & 0xfffffu) <= 6u || __builtin_fabsf(y[j]) < 0x1p-6f;
-    }
-    if (redo && mx) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[j] / sc;
-    }
-    uint2v o;
+    for (int j = 0; j < 8; ++j) t[j] = x[j] * inv;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+        o[h] = code4(t[4 * h] * (1.f - EPS), t[4 * h + 1] * (1.f - EPS), t[4 * h + 2] * (1.f - EPS), t[4 * h + 3] * (1.f - EPS));
+        o2[h] = code4(t[4 * h] * (1.f + EPS), t[4 * h + 1] * (1.f + EPS), t[4 * h + 2] * (1.f + EPS), t[4 * h + 3] * (1.f + EPS));
+    }
+    // (a scale so small that its inverse may overflow: every value)
+    const bool small = sc < 0x1p-100f && sc > 0.0f;
+    if (o.x != o2.x || o.y != o2.y || small) {
+        float xg[8];
+        if (SWIGLU) widen8<BF16>(g, xg);
 #pragma unroll
-        for (int j = 4 * h; j < 4 * h + 4; ++j)
-            // (a NaN passes both comparisons)
-            y[j] = y[j] > 448.f ? 448.f : y[j] < -448.f ? -448.f : y[j];
-        int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h], y[4 * h + 1], 0, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h + 2], y[4 * h + 3], w, true);
-        o[h] = (unsigned)w;
+        for (int j = 0; j < 8; ++j) {
+            const unsigned differ = (o[j / 4] ^ o2[j / 4]) >> (8 * (j & 3)) & 0xffu;
+            if (differ || small) {
+                const float v = SWIGLU ? (float)(silu_64(xg[j], y[j]) / (double)sc) : x[j] / sc;
+                const unsigned c = code4(v > 448.f ? 448.f : v < -448.f ? -448.f : v, 0.f, 0.f, 0.f) & 0xffu;
+                o[j / 4] = (o[j / 4] & ~(0xffu << (8 * (j & 3)))) | c << (8 * (j & 3));
+            }
+        }
     }
     __builtin_nontemporal_store(o, reinterpret_cast<uint2v *>(Aq + at));
 }
+#undef QG_ROW_MAX
+#undef QG_ROT_MAX
 
 } // namespace
 
