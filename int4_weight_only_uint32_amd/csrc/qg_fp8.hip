@@ -20,6 +20,9 @@ constexpr int KB8 = 128;   // k extent of a scale block, bytes of a tile row
 // An offset past every buffer range here (at most 2^32 - 2^23 bytes, which the
 // caller checks), also after a step's scalar offset (below 2^22 + 256) is added.
 constexpr unsigned FP8_PAST = 0xFFBFFFF0u - 0x1000u;
+// The same for a tile of W: at most 256 rows, 2^30 bytes, and scalar offsets
+// up to such a tile.
+constexpr unsigned FP8_W_PAST = 0x80000000u;
 
 // The BM-row blocks of all experts, in order, and the one an index names.  The
 // counts stand in the device's offsets, so the grid is an upper bound and every
@@ -125,8 +128,11 @@ __device__ inline void store4(uint16_t *c, float4v x, bool zero, int n, int N, b
 // to LDS, double-buffered, one barrier a step.  In LDS, 16-byte chunk c of row r
 // stands at position c ^ (r % 8), so that the 16 rows a wave reads at once
 // spread over the banks.
-template <int BM, int BN, int WM, int WN, bool BF16>
-__global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
+// KS > 1: KS such groups of waves, each with LDS of its own, take the steps in
+// turn, and their sums meet in LDS in the order of the groups; for grids that
+// leave CUs idle or K long, where a step's latency is what counts.
+template <int BM, int BN, int WM, int WN, int KS, bool BF16>
+__global__ __launch_bounds__(64 * WM * WN * KS) void fp8_tiled_kernel(
     const uint8_t *__restrict__ Aall, const float *__restrict__ a_scale,
     const int32_t *__restrict__ a_rows, int M_a, const uint8_t *__restrict__ Wall,
     const float *__restrict__ Sall, const int32_t *__restrict__ offsets, int E, int M, int N,
@@ -136,7 +142,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     constexpr int LA = BM / 8 / NW, LW = BN / 8 / NW;    // 1 KB loads per wave and step
     static_assert(LA * NW * 8 == BM && LW * NW * 8 == BN, "whole loads per wave");
     static_assert(BN / WN <= 128 && 128 % (BN / WN) == 0, "a wave's columns share one weight scale");
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds_all[];
     constexpr int STAGE = (BM + BN) * KB8;
 
     int rb, n0;
@@ -148,8 +154,12 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     const int m0 = __builtin_amdgcn_readfirstlane(blk.m0);
     const int m1 = __builtin_amdgcn_readfirstlane(blk.m1);
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = KS > 1 ? wave_all / NW : 0, wave = KS > 1 ? wave_all % NW : wave_all;
     const int wm = wave / WN, wn = wave % WN;
+    uint8_t *lds = lds_all + group * (2 * STAGE);
+    // this group's steps: kt stands for k block kt * KS + group
+    const int steps = (KB + KS - 1) / KS;
 
     // every lane's source chunk within a row, and its rows' byte offsets; rows
     // past the end read the last row (never stored)
@@ -159,7 +169,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     const __amdgpu_buffer_rsrc_t w_rs = buffer_rsrc(W, (size_t)rows_n * K);
     const __amdgpu_buffer_rsrc_t a_rs =
         a_rows ? buffer_rsrc(Aall, (size_t)M_a * K) : buffer_rsrc(Aall + (size_t)m0 * K, (size_t)(m1 - m0) * K);
-    unsigned a_off[LA], w_off[LW];
+    unsigned a_off[LA];
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
         int r = (wave * LA + i) * 8 + (lane >> 3);
@@ -170,12 +180,8 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
         }
         a_off[i] = (unsigned)r * (unsigned)K + chunk * 16;
     }
-#pragma unroll
-    for (int i = 0; i < LW; ++i) {
-        int r = (wave * LW + i) * 8 + (lane >> 3);
-        r = r < rows_n ? r : rows_n - 1;
-        w_off[i] = (unsigned)r * (unsigned)K + chunk * 16;
-    }
+    // (rows of W past N read nothing: zeros, never stored)
+    const unsigned w_off = (unsigned)(wave * LW * 8 + (lane >> 3)) * (unsigned)K + chunk * 16;
     // Every load of step kt.  Chunks past the end of K (in the last step of a
     // K that is no multiple of 128, and in the steps past the last that the loop
     // below asks for without a branch) take an offset beyond every range, which
@@ -186,33 +192,44 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     // launch stub)
     constexpr int PIECES = LA + LW;
     auto load_piece = [&](int kt, int q) {
-        const bool in = kt * KB8 + chunk * 16 < K;
-        unsigned off = in ? (q < LA ? a_off[q] : w_off[q - LA]) : FP8_PAST;
-        pin(off);        // one load for all lanes, not two under half an exec mask
-        uint8_t *dst = lds + (kt & 1) * STAGE + (q < LA ? wave * LA + q : BM / 8 + wave * LW + q - LA) * 1024;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(q < LA ? a_rs : w_rs, (__attribute__((address_space(3))) void *)dst, 16, off, kt * KB8, 0, 0);
+        const int k = (kt * KS + group) * KB8;
+        const bool in = k + chunk * 16 < K;
+        // (pinned: one load for all lanes, not two under half an exec mask)
+        if (q < LA) {
+            unsigned off = in ? a_off[q] : FP8_PAST;
+            pin(off);
+            uint8_t *dst = lds + (kt & 1) * STAGE + (wave * LA + q) * 1024;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rs, (__attribute__((address_space(3))) void *)dst, 16, off, k, 0, 0);
+        } else {
+            unsigned off = in ? w_off : FP8_W_PAST;
+            pin(off);
+            uint8_t *dst = lds + (kt & 1) * STAGE + (BM / 8 + wave * LW + q - LA) * 1024;
+            const int more = k + (q - LA) * 8 * K;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rs, (__attribute__((address_space(3))) void *)dst, 16, off, more, 0, 0);
+        }
     };
 
     // Scales, four steps at a time: lane l loads, for its row (l % 16) of each
     // m-tile, the scale of step 4 c + l / 16, so one 4-byte load a row serves
     // four steps (a load for every step asks L2 for a whole line per row each
     // time: 52 of 278 us at 4096 x 8192 x 8192).  The product with the
-    // weight block's scale is then handed to the four lanes of a row by a
-    // lane permute.
-    unsigned s_off[MT];
-    bool bad[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        int r = (wm * MT + t) * 16 + (lane & 15);
-        r = m0 + r < m1 ? r : m1 - 1 - m0;
-        bad[t] = false;
+    // weight block's scale is then handed to the four lanes of a row through
+    // LDS.
+    // The rows' scale offsets stand in LDS, where they cost no registers of the main
+    // loop; bit 0 marks a row of no activations.
+    unsigned *s_tab = reinterpret_cast<unsigned *>(lds_all + KS * 2 * STAGE);
+    for (int i = threadIdx.x; i < BM; i += 64 * NW * KS) {
+        int r = m0 + i < m1 ? i : m1 - 1 - m0;
+        bool none = false;
         if (a_rows) {
             r = a_rows[m0 + r];
-            bad[t] = (unsigned)r >= (unsigned)M_a;
-            r = bad[t] ? 0 : r;
+            none = (unsigned)r >= (unsigned)M_a;
+            r = none ? 0 : r;
         }
-        s_off[t] = ((unsigned)r * (unsigned)KB + (lane >> 4)) * 4u;
+        s_tab[i] = (unsigned)r * (unsigned)KB * 4u | (none ? 1u : 0u);
     }
+    __syncthreads();
+    const int my_row = wm * MT * 16 + (lane & 15);     // of m-tile 0
     const __amdgpu_buffer_rsrc_t sa_rs = a_rows ? buffer_rsrc(a_scale, (size_t)M_a * KB * 4)
                                                 : buffer_rsrc(a_scale + (size_t)m0 * KB, (size_t)(m1 - m0) * KB * 4);
     int nb = (n0 + wn * NT * 16) / 128;
@@ -244,23 +261,29 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     // landed, and its first operands are read between the last MFMAs.  The
     // scheduling barriers keep this order.
     float sa[MT], sb;             // scales of the next four steps, in flight
-    float four[MT];               // products of the scales of four steps
     float s[MT], s_old[MT];       // this step's, and those of the step whose last results wait
     float4v p[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) p[t] = float4v{0.f, 0.f, 0.f, 0.f};
     auto load_scales = [&](int c) {
-        sb = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sw_rs, (lane >> 4) * 4, c * 16, 0));
+        // (with KS > 1 a block past the last may be multiplied: its scale is 0; with
+        // one group it never is)
+        const bool in = KS == 1 || (c * 4 + (lane >> 4)) * KS + group < KB;
+        const unsigned o = in ? (unsigned)((lane >> 4) * KS + group) * 4u : FP8_PAST;
+        sb = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sw_rs, o, c * 16 * KS, 0));
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            const unsigned o = s_off[t];
-            sa[t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sa_rs, o, c * 16, 0));
+            const unsigned os = in ? (s_tab[my_row + 16 * t] & ~1u) + ((lane >> 4) * KS + group) * 4 : FP8_PAST;
+            sa[t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(sa_rs, os, c * 16 * KS, 0));
         }
     };
-    auto of_step = [&](float x, int kt) {     // the value of lane group kt % 4
-        const int from = ((kt & 3) * 16 + (lane & 15)) * 4;
-        return __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, x)));
+    // the products of the scales of four steps, [m-tile][step][row] of this wave's own
+    float *four = reinterpret_cast<float *>(lds_all + KS * 2 * STAGE + BM * 4) + wave_all * (MT * 64);
+    auto keep_scales = [&]() {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) four[t * 64 + lane] = sa[t] * sb;
     };
+    auto of_step = [&](int t, int at) { return four[t * 64 + (at & 3) * 16 + (lane & 15)]; };
     if (m0 + wm * MT * 16 >= m1) {
         // None of this wave's rows exist (the last block of an expert's rows): it
         // keeps loading and meeting the others at the barriers, and leaves the
@@ -271,7 +294,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < PIECES; ++q) load_piece(1, q);
-        for (int kt = 0; kt < KB; ++kt) {
+        for (int kt = 0; kt < steps; ++kt) {
             __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
             __syncthreads();
 #pragma unroll
@@ -279,6 +302,10 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
         }
         __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
         __syncthreads();
+        if (KS > 1) {
+            __syncthreads();
+            __syncthreads();
+        }
         return;
     }
     load_scales(0);
@@ -287,11 +314,10 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     __syncthreads();
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-        four[t] = sa[t] * sb;
-        s[t] = of_step(four[t], 0);
-        s_old[t] = 0.f;
-    }
+    for (int t = 0; t < MT; ++t) s_old[t] = 0.f;
+    keep_scales();
+#pragma unroll
+    for (int t = 0; t < MT; ++t) s[t] = of_step(t, 0);
     // Loads go out one behind each of the first MFMAs after the barrier: in one
     // burst behind it they hold every wave's issue until the address unit has
     // taken them (289 against 278 us at 4096 x 8192 x 8192), and further apart
@@ -318,11 +344,9 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
                 __builtin_amdgcn_s_waitcnt(0);
                 debug_stage_sync();
                 __syncthreads();
+                if (at == 3) keep_scales();
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    if (at == 3) four[t] = sa[t] * sb;
-                    s_new[t] = of_step(four[t], at + 1);
-                }
+                for (int t = 0; t < MT; ++t) s_new[t] = of_step(t, at + 1);
                 if (at == 2) load_scales((kt >> 2) + 1);
                 w[0] = operand(nxt + w_base);      // (stale data after the last step, unused)
             } else {
@@ -349,18 +373,23 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
             s[t] = s_new[t];
         }
     };
-    // (four steps to a round, for the scales; no branch inside a step: the
-    // compiler would sink the FMAs before it to where it joins again, and keep
-    // all products alive)
-    for (int kt = 0;; kt += 4) {
+    // Four steps to a round, for the scales, then the up to three left over.  (No
+    // branch inside a step, where the compiler would sink the FMAs before it to
+    // where it joins again and keep all products alive, and no way out of the
+    // middle of a round, which costs copies of the accumulators.)
+    int kt = 0;
+    for (; kt + 4 <= steps; kt += 4) {
         step(kt, 0);
-        if (kt + 1 >= KB) break;
         step(kt + 1, 1);
-        if (kt + 2 >= KB) break;
         step(kt + 2, 2);
-        if (kt + 3 >= KB) break;
         step(kt + 3, 3);
-        if (kt + 4 >= KB) break;
+    }
+    if (kt < steps) {
+        step(kt, 0);
+        if (kt + 1 < steps) {
+            step(kt + 1, 1);
+            if (kt + 2 < steps) step(kt + 2, 2);
+        }
     }
 #pragma unroll
     for (int u = MT * NT - 2; u < MT * NT; ++u)
@@ -376,7 +405,29 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     __syncthreads();
     constexpr int ROW = NT * 16 * 2, CH = ROW / 16, RPI = 64 / CH;   // bytes and chunks of a row, rows of one store
     static_assert(MT * 16 * ROW * NW <= 2 * STAGE && CH >= 2 && CH <= 16, "the tile fits, a row in 16 chunks");
+    if (KS > 1) {
+        constexpr int PART = MT * NT * NW * 64;       // float4 of one group
+        static_assert((KS - 1) * PART * 16 <= KS * 2 * STAGE, "the groups' sums fit");
+        float4v *part = reinterpret_cast<float4v *>(lds_all);
+        if (group > 0) {
+#pragma unroll
+            for (int t = 0; t < MT * NT; ++t)
+                part[(group - 1) * PART + (t * NW + wave) * 64 + lane] = acc[t / NT][t % NT];
+        }
+        __syncthreads();
+        if (group == 0) {
+#pragma unroll
+            for (int g = 1; g < KS; ++g)
+#pragma unroll
+                for (int t = 0; t < MT * NT; ++t) acc[t / NT][t % NT] += part[(g - 1) * PART + (t * NW + wave) * 64 + lane];
+        }
+        __syncthreads();
+        if (group > 0) return;
+    }
     const int row0 = m0 + wm * MT * 16, col0 = n0 + wn * NT * 16;
+    bool bad[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) bad[i] = s_tab[my_row + 16 * i] & 1u;
     if (N % 8 == 0 && ((uintptr_t)C & 15) == 0) {
         uint8_t *mine = lds + wave * (MT * 16 * ROW);
 #pragma unroll
@@ -603,7 +654,10 @@ long long row_blocks(bool grouped, int E, int M, int BM)
 
 // The kernel of a call: the streaming ones by their m-tiles, n-tiles and waves,
 // the tiled ones by their tile.
-enum Fp8Kernel { S1x2x4, S1x2x2, S1x1x4, S2x2x4, S2x4x2, S4x2x4, S4x4x4, T64x128, T256x256 };
+enum Fp8Kernel {
+    S1x2x4, S1x2x2, S1x1x4, S2x2x4, S2x4x2, S4x2x4, S4x4x4,
+    T64x64K2, T64x128, T64x128K2, T128x128K2, T128x256, T256x256
+};
 
 struct Fp8Shape {
     const char *name;
@@ -613,8 +667,10 @@ constexpr Fp8Shape FP8_SHAPES[] = {
     {"streaming, 16 x 32, 4 waves over k", 16, 32, 256},  {"streaming, 16 x 32, 2 waves over k", 16, 32, 128},
     {"streaming, 16 x 16, 4 waves over k", 16, 16, 256},  {"streaming, 32 x 32, 4 waves over k", 32, 32, 256},
     {"streaming, 32 x 64, 2 waves over k", 32, 64, 128},  {"streaming, 64 x 32, 4 waves over k", 64, 32, 256},
-    {"streaming, 64 x 64, 4 waves over k", 64, 64, 256},  {"tiled, 64 x 128", 64, 128, 256},
-    {"tiled, 256 x 256", 256, 256, 512}};
+    {"streaming, 64 x 64, 4 waves over k", 64, 64, 256},
+    {"tiled, 64 x 64, 2 groups over k", 64, 64, 512},     {"tiled, 64 x 128", 64, 128, 256},
+    {"tiled, 64 x 128, 2 groups over k", 64, 128, 512},   {"tiled, 128 x 128, 2 groups over k", 128, 128, 512},
+    {"tiled, 128 x 256", 128, 256, 256},                  {"tiled, 256 x 256", 256, 256, 512}};
 
 // By the rows an expert has on average (the host does not know the counts; an
 // uneven split is slower, never wrong) and the workgroups that makes.  Both
@@ -636,29 +692,46 @@ Fp8Kernel choose(bool grouped, int E, int M, int N, int K)
     // 32 rows: 27.2, as two blocks of 16 35.0, tiled 44.4; 16 rows an
     // expert in 64 experts at 2048 x 7168: 174 (32 x 64) against 225 (32 x 32)
     if (rows <= 32) return wgs(32, 32) >= 2048 ? S2x4x2 : S2x2x4;
-    // 64 rows: 39.7 (64 columns), 42.7 (32 columns), tiled 45.3; at 17408 x 5120
-    // 56.7, 42.9 and 134.  Many experts fill the chip without the split over k: 32
-    // rows an expert in 64 experts at 2048 x 7168: 197 tiled, 228 streaming
-    if (rows <= 64 && wgs(64, 128) < 1024) return wgs(64, 64) >= 256 ? S4x4x4 : S4x2x4;
-    // 512 rows (136 tiles of 256 x 256): 88 against 103 for 64 x 128; 256 rows (68
-    // tiles): 89 against 67; 512 rows at 17408 x 5120 (40 tiles): 249 against 142
-    if (rows > 128 && wgs(256, 256) >= 128) return T256x256;
+    const long long w64 = wgs(64, 128), w128 = wgs(128, 128), w256 = wgs(256, 256);
+    if (rows <= 128 && w64 <= 128) {
+        // Few tiles: the streaming kernels make more workgroups.  64 rows at 17408 x
+        // 5120: 42.8, 64 x 64 tiles 63.7; 128 rows there: 55 (64 columns), 62; 100 rows at
+        // 640 x 1000: 4.6, tiled 5.0
+        if (rows <= 64 || K <= 4096) return S4x2x4;
+        return S4x4x4;
+    }
+    if (rows > 128) {
+        // 512 rows (136 large tiles): 88 against 103 for 64 x 128; 256 rows (136 tiles
+        // of 128 x 256): 61 against 66 and 82 (68 large tiles); 2000 rows at 4096 x 4096
+        // (256 or 128): 40 against 51
+        const long long w = wgs(128, 256);
+        if (w256 >= 192 || (w256 >= 128 && w > 256)) return T256x256;
+        if (w > 128 && w <= 256) return T128x256;
+    }
+    // One tile to a CU at most: two groups over k.  256 rows at 4096 x 8192 (256 tiles):
+    // 18.6 against 22.3; 64 rows (136): 34.4, 40.7, streaming 39.8; 300 rows at 2000 x
+    // 3000 (235 tiles of 64 x 64): 10 against 14
+    if (w64 <= 128) return T64x64K2;
+    if (w64 <= 256) return T64x128K2;
+    // 128 rows (136 tiles): 43 against 52; 512 rows at 17408 x 5120 (160): 115, 135
+    if (rows > 64 && w128 <= 256) return T128x128K2;
+    // (up to 128 rows an expert, many tiles)
     return T64x128;
 }
 
 // The tiled kernel on columns col_first .. col_end - 1 (col_first a multiple of 128).
-template <int BM, int BN, int WM, int WN, bool BF16>
+template <int BM, int BN, int WM, int WN, int KS, bool BF16>
 hipError_t tiled(const Fp8Args &a, int col_first, int col_end, hipStream_t st)
 {
-    const auto kern = fp8_tiled_kernel<BM, BN, WM, WN, BF16>;
-    constexpr int bytes = 2 * (BM + BN) * KB8;
+    const auto kern = fp8_tiled_kernel<BM, BN, WM, WN, KS, BF16>;
+    constexpr int bytes = KS * (2 * (BM + BN) * KB8 + WM * WN * (BM / WM / 16) * 256) + BM * 4;
     if (bytes > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
     const int nbn = (col_end - col_first + BN - 1) / BN;
     const long long wgs = row_blocks(a.offsets != nullptr, a.E, a.M, BM) * nbn;
-    hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(64 * WM * WN), bytes, st, a.A, a.a_scale, a.a_rows,
+    hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(64 * WM * WN * KS), bytes, st, a.A, a.a_scale, a.a_rows,
                        a.M_a, a.W, a.w_scale, a.offsets, a.E, a.M, a.N, a.K, a.KB, a.NB, col_first, nbn, a.C);
     return hipGetLastError();
 }
@@ -701,12 +774,16 @@ hipError_t launch(const Fp8Args &a, hipStream_t st)
     case S2x4x2: return stream<2, 4, 2, 2, BF16>(a, st);
     case S4x2x4: return stream<4, 2, 4, 2, BF16>(a, st);
     case S4x4x4: return stream<4, 4, 4, 2, BF16>(a, st);
-    case T64x128: return tiled<64, 128, 2, 2, BF16>(a, 0, a.N, st);
+    case T64x64K2: return tiled<64, 64, 2, 2, 2, BF16>(a, 0, a.N, st);
+    case T64x128: return tiled<64, 128, 2, 2, 1, BF16>(a, 0, a.N, st);
+    case T64x128K2: return tiled<64, 128, 2, 2, 2, BF16>(a, 0, a.N, st);
+    case T128x128K2: return tiled<128, 128, 2, 2, 2, BF16>(a, 0, a.N, st);
+    case T128x256: return tiled<128, 256, 2, 2, 1, BF16>(a, 0, a.N, st);
     case T256x256: {
         const int end = large_cols(a) * 256;
-        if (end >= a.N) return tiled<256, 256, 4, 2, BF16>(a, 0, a.N, st);
-        const hipError_t e = tiled<256, 256, 4, 2, BF16>(a, 0, end, st);
-        return e != hipSuccess ? e : tiled<128, 128, 2, 2, BF16>(a, end, a.N, st);
+        if (end >= a.N) return tiled<256, 256, 4, 2, 1, BF16>(a, 0, a.N, st);
+        const hipError_t e = tiled<256, 256, 4, 2, 1, BF16>(a, 0, end, st);
+        return e != hipSuccess ? e : tiled<128, 128, 2, 2, 1, BF16>(a, end, a.N, st);
     }
     }
     return hipErrorUnknown;

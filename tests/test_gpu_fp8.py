@@ -200,13 +200,20 @@ def test_dense(M, N, K, dtype):
     check(C, *dequant(a, sa, w, sw), dtype)
 
 
-# one shape or two of every kernel the rule on rows and workgroups can choose that
-# the small shapes above do not reach (its thresholds: 16, 32, 64 and 128 rows,
-# 128, 256, 1024 and 2048 workgroups, K 4096)
-@pytest.mark.parametrize("M,N,K", [
+# shapes for every kernel that the rule on rows and workgroups can choose, on
+# both sides of its thresholds (rows 16, 32, 64, 128; workgroups 128, 192, 256, 2048;
+# K 4096), with one k block, odd numbers of them and partial ones
+WIDE = [
     (3, 65540, 272), (16, 65600, 4112), (9, 4100, 4112), (16, 4096, 1040), (20, 65600, 272), (32, 70000, 144),
-    (40, 16400, 272), (64, 16384, 1168), (50, 8200, 4112), (300, 16500, 400), (512, 17408, 5120), (1025, 8196, 656),
-    (1000, 17500, 272), (1024, 17408, 144)])        # columns left over from whole rounds of the large tile
+    (40, 4100, 272), (64, 5120, 4240), (100, 4100, 4240), (128, 2050, 1168), (50, 16500, 400), (64, 20000, 128),
+    (128, 8200, 656), (100, 17408, 1296), (128, 20000, 80), (200, 3000, 2000), (300, 3000, 112), (290, 5000, 656),
+    (256, 8192, 784), (300, 17000, 400), (512, 9000, 128), (500, 8200, 912), (700, 2050, 1152), (2000, 4096, 272),
+    (260, 17500, 272), (512, 17408, 5120), (1025, 8196, 656), (1300, 6000, 400), (900, 4700, 144),
+    (40, 33500, 144), (100, 33500, 272),
+    (1000, 17500, 272), (1024, 17408, 144)]          # the last two: columns left over from whole rounds
+
+
+@pytest.mark.parametrize("M,N,K", WIDE)
 def test_dense_wide(M, N, K):
     note(f"fp8_gemm M={M} N={N} K={K}")
     a, w = codes((M, K), 1), codes((N, K), 2)
