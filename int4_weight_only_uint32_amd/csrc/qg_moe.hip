@@ -224,7 +224,7 @@ __device__ inline float route_error(bool sigmoid, float c)
 }
 
 template <int VPL>
-__global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, int gl_shift)
+__global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, int gl_shift, int size, int size_magic)
 {
     __shared__ double sh[4][VPL * 64];
     const int lane = threadIdx.x & 63;
@@ -317,25 +317,48 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
             }
         }
     }
-    bool unsure = false, keep = true;
+    bool unsure = false;
+    unsigned keep = ~0u;       // bit i: this lane's expert i is in a group that stays
     if (a.n_group > 1) {
-        // 2^gl_shift lanes to a group: its two largest values, then how many
-        // groups are above it
+        // The two largest values of each group.  Groups on whole runs of a power of
+        // two lanes (gl_shift >= 0): in all lanes of the run, by exchanges; others: in
+        // lane g for group g, out of LDS.
         float v1 = NINF, v2 = NINF;
+        int mine = lane, stride = 0;       // this lane's group, its first lane's shift
+        if (gl_shift >= 0) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            v2 = __builtin_fmaxf(v2, __builtin_fminf(v1, v[i]));
-            v1 = __builtin_fmaxf(v1, v[i]);
+            for (int i = 0; i < VPL; ++i) {
+                v2 = __builtin_fmaxf(v2, __builtin_fminf(v1, v[i]));
+                v1 = __builtin_fmaxf(v1, v[i]);
+            }
+            for (int o = 0; o < gl_shift; ++o) {
+                const float u = __shfl_xor(v1, 1 << o), u2 = __shfl_xor(v2, 1 << o);
+                v2 = __builtin_fmaxf(__builtin_fminf(v1, u), __builtin_fmaxf(v2, u2));
+                v1 = __builtin_fmaxf(v1, u);
+            }
+            mine = lane >> gl_shift;
+            stride = gl_shift;
+        } else {
+            float *vals = reinterpret_cast<float *>(sh[wave]);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) vals[e0 + i] = v[i];
+            // (the wave's own words, in order: no other wave to wait for)
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            if (lane < a.n_group)
+                for (int j = 0; j < size; ++j) {
+                    const float x = vals[lane * size + j];
+                    v2 = __builtin_fmaxf(v2, __builtin_fminf(v1, x));
+                    v1 = __builtin_fmaxf(v1, x);
+                }
+            __builtin_amdgcn_wave_barrier();
         }
-        for (int o = 0; o < gl_shift; ++o) {
-            const float u = __shfl_xor(v1, 1 << o), u2 = __shfl_xor(v2, 1 << o);
-            v2 = __builtin_fmaxf(__builtin_fminf(v1, u), __builtin_fmaxf(v2, u2));
-            v1 = __builtin_fmaxf(v1, u);
-        }
-        const int mine = lane >> gl_shift;
+        const bool group = mine < a.n_group;
         auto group_value = [&](int g) {
-            return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v1), g << gl_shift));
+            return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v1), g << stride));
         };
+        bool stays;
         if (scored) {
             // twice the largest error of a value, so that values further apart
             // than it are in order
@@ -354,17 +377,28 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
                 above += x > hi;
                 not_below += x >= lo;
             }
-            unsure = __ballot(mine < a.n_group && above < a.topk_group && not_below >= a.topk_group) != 0;
-            keep = not_below < a.topk_group;
+            unsure = __ballot(group && above < a.topk_group && not_below >= a.topk_group) != 0;
+            stays = not_below < a.topk_group;
         } else {
             int before = 0;
             for (int g = 0; g < a.n_group; ++g) {
                 const float x = group_value(g);
                 before += x > v1 || (x == v1 && g < mine);
             }
-            keep = before < a.topk_group;
+            stays = before < a.topk_group;
         }
-        keep = keep && mine < a.n_group;
+        stays = stays && group;
+        if (gl_shift >= 0) {
+            keep = stays ? ~0u : 0u;
+        } else {
+            const unsigned long long groups = __ballot(stays);
+            keep = 0;
+            // e / size for e < 1024 as e * ceil(2^20 / size) >> 20: off by less than
+            // 1024 / 2^20 of the quotient, and size is at most 512
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                keep |= (unsigned)((groups >> (((e0 + i) * size_magic >> 20) & 63)) & 1) << i;
+        }
     }
     // Each lane's keys (0 for a masked expert) in descending order, the lower
     // index first among equals (neighbours change places only if out of order),
@@ -373,7 +407,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
     unsigned key[VPL], idx[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        key[i] = keep && c[i] > NINF ? order_key(c[i]) : 0u;
+        key[i] = (keep >> i & 1) && c[i] > NINF ? order_key(c[i]) : 0u;
         idx[i] = i;
     }
 #pragma unroll
@@ -437,16 +471,6 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
     float w = s * a.scaling;
     if (renorm) w = sum > 0.f ? s / sum * a.scaling : 0.f;
     route_store(a, t, lane, my_id, w);
-}
-
-// Groups that do not lie on whole runs of a power of two lanes: in 64 bits.
-template <int VPL>
-__global__ __launch_bounds__(256) void moe_route_exact_kernel(RouteArgs a)
-{
-    __shared__ double sh[4][VPL * 64];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int t = blockIdx.x * 4 + wave;
-    if (t < a.T) route_exact<VPL>(a, t, sh[wave]);
 }
 
 // ---- sort ----
@@ -704,15 +728,12 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t st)
 {
     const dim3 grid((a.T + 3) / 4), block(256);
     const int size = a.E / a.n_group, gl = size / VPL;
-    if (a.n_group > 1 && (size % VPL != 0 || (gl & (gl - 1)) != 0)) {
-        hipLaunchKernelGGL((moe_route_exact_kernel<VPL>), grid, block, 0, st, a);
-    } else {
-        const size_t bytes = (size_t)VPL * (a.dtype == QG_DT_F32 ? 4 : 2);
-        const int wide = a.E % VPL == 0 && (uintptr_t)a.logits % bytes == 0 && (uintptr_t)a.bias % (VPL * 4) == 0;
-        int shift = 0;
-        while ((1 << shift) < gl) ++shift;
-        hipLaunchKernelGGL((moe_route_kernel<VPL>), grid, block, 0, st, a, wide, shift);
-    }
+    const size_t bytes = (size_t)VPL * (a.dtype == QG_DT_F32 ? 4 : 2);
+    const int wide = a.E % VPL == 0 && (uintptr_t)a.logits % bytes == 0 && (uintptr_t)a.bias % (VPL * 4) == 0;
+    int shift = 0;
+    while ((1 << shift) < gl) ++shift;
+    if (size % VPL != 0 || (1 << shift) != gl) shift = -1;
+    hipLaunchKernelGGL((moe_route_kernel<VPL>), grid, block, 0, st, a, wide, shift, size, ((1 << 20) + size - 1) / size);
     return hipGetLastError();
 }
 } // namespace
