@@ -43,46 +43,56 @@ __device__ inline void expert_rows(const int32_t *__restrict__ offsets, int E, i
     }
 }
 
-__device__ inline int row_block_count(const int32_t *__restrict__ offsets, int E, int M, int BM)
+// Inclusive scan of the row blocks of 64 experts from e0 on, one a lane.
+struct RowScan {
+    int r0, r1, blocks, sum;
+};
+
+__device__ inline RowScan scan_rows(const int32_t *__restrict__ offsets, int E, int M, int BM, int e0)
 {
-    if (!offsets) return (M + BM - 1) / BM;
-    int n = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        int r0, r1;
-        expert_rows(offsets, E, M, e0 + (threadIdx.x & 63), r0, r1);
-        n += (r1 - r0 + BM - 1) / BM;
-    }
+    const int lane = threadIdx.x & 63;
+    RowScan s;
+    expert_rows(offsets, E, M, e0 + lane, s.r0, s.r1);
+    s.blocks = (s.r1 - s.r0 + BM - 1) / BM;
+    s.sum = s.blocks;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
-    return __builtin_amdgcn_readfirstlane(n);
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(s.sum, o);
+        if (lane >= o) s.sum += v;
+    }
+    return s;
 }
 
-// Row block rb of row_block_count's (rb below it).
+__device__ inline int row_block_count(const int32_t *__restrict__ offsets, int E, int M, int BM,
+                                      const RowScan &first)
+{
+    if (!offsets) return (M + BM - 1) / BM;
+    int n = __builtin_amdgcn_readlane(first.sum, 63);
+    for (int e0 = 64; e0 < E; e0 += 64)
+        n += __builtin_amdgcn_readlane(scan_rows(offsets, E, M, BM, e0).sum, 63);
+    return n;
+}
+
+// Row block rb; {0, 0, 0} if there are fewer.  first: scan_rows from expert 0 on.
 __device__ inline RowBlock find_rows(const int32_t *__restrict__ offsets, int E, int M, int BM,
-                                     int rb)
+                                     int rb, const RowScan &first)
 {
     if (!offsets) return RowBlock{0, rb * BM, M};
-    const int lane = threadIdx.x & 63;
+    RowScan s = first;
     int base = 0;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        int r0, r1;
-        expert_rows(offsets, E, M, e0 + lane, r0, r1);
-        const int nb = (r1 - r0 + BM - 1) / BM;
-        int sum = nb;      // inclusive scan
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(sum, o);
-            if (lane >= o) sum += v;
-        }
-        const unsigned long long hit = __ballot(base + sum > rb);
+    for (int e0 = 0;;) {
+        const unsigned long long hit = __ballot(base + s.sum > rb);
         if (hit) {
             const int l = __builtin_ctzll(hit);
-            const int first = base + __shfl(sum - nb, l);
-            return RowBlock{e0 + l, __shfl(r0, l) + (rb - first) * BM, __shfl(r1, l)};
+            const int before = base + __builtin_amdgcn_readlane(s.sum - s.blocks, l);
+            return RowBlock{e0 + l, __builtin_amdgcn_readlane(s.r0, l) + (rb - before) * BM,
+                            __builtin_amdgcn_readlane(s.r1, l)};
         }
-        base += __shfl(sum, 63);
+        base += __builtin_amdgcn_readlane(s.sum, 63);
+        e0 += 64;
+        if (e0 >= E) return RowBlock{0, 0, 0};
+        s = scan_rows(offsets, E, M, BM, e0);
     }
-    return RowBlock{0, 0, 0};
 }
 
 // The tile of workgroup b out of rbs row blocks x nbn column blocks, false if
@@ -147,9 +157,11 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void fp8_tiled_kernel(
 
     int rb, n0;
     // uniform over the workgroup, before any barrier
-    if (!tile_of<1024 / BM>(blockIdx.x, row_block_count(offsets, E, M, BM), nbn, rb, n0)) return;
+    RowScan scan = {};
+    if (offsets) scan = scan_rows(offsets, E, M, BM, 0);
+    if (!tile_of<1024 / BM>(blockIdx.x, row_block_count(offsets, E, M, BM, scan), nbn, rb, n0)) return;
     n0 = col_first + n0 * BN;
-    const RowBlock blk = find_rows(offsets, E, M, BM, rb);
+    const RowBlock blk = find_rows(offsets, E, M, BM, rb, scan);
     const int e = __builtin_amdgcn_readfirstlane(blk.e);
     const int m0 = __builtin_amdgcn_readfirstlane(blk.m0);
     const int m1 = __builtin_amdgcn_readfirstlane(blk.m1);
@@ -259,7 +271,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void fp8_tiled_kernel(
     // column tile.  There every operand of the step is in registers, so behind it
     // the step's buffer is filled again (for step k + 2), step k + 1's tiles have
     // landed, and its first operands are read between the last MFMAs.  The
-    // scheduling barriers keep this order.
+    // scheduling barriers and the pinned values keep this order (without the pins the
+    // compiler delays FMAs, keeps their products alive and spills).
     float sa[MT], sb;             // scales of the next four steps, in flight
     float s[MT], s_old[MT];       // this step's, and those of the step whose last results wait
     float4v p[4];
@@ -357,10 +370,12 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void fp8_tiled_kernel(
             for (int i = 0; i < MT; ++i) {
                 const int t = j * MT + i, u = t - 2;      // this tile, the tile folded now
                 p[t & 3] = mfma_fp8(w[j & 1], a[i], float4v{0.f, 0.f, 0.f, 0.f});
+                pin(p[t & 3]);
                 const int ui = u < 0 ? (u + MT * NT) % MT : u % MT, uj = u < 0 ? (u + MT * NT) / MT : u / MT;
                 const float us = u < 0 ? s_old[ui] : s[ui];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[ui][uj][r] = __builtin_fmaf(p[u & 3][r], us, acc[ui][uj][r]);
+                pin(acc[ui][uj]);
                 const int slot = j == NT - 1 ? i : (j + 1) * MT + i;
                 if (slot < PIECES) load_piece(j == NT - 1 ? kt + 2 : kt + 1, slot);
                 if (j == NT - 1) a[i] = operand(nxt + a_base + i * 16 * KB8);
@@ -499,7 +514,9 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int nbn = (N + BN - 1) / BN;
     const int rb = blockIdx.x / nbn, n0 = (blockIdx.x - rb * nbn) * BN;
-    const RowBlock blk = find_rows(offsets, E, M, BM, rb);
+    RowScan scan = {};
+    if (offsets) scan = scan_rows(offsets, E, M, BM, 0);
+    const RowBlock blk = find_rows(offsets, E, M, BM, rb, scan);
     const int e = __builtin_amdgcn_readfirstlane(blk.e);
     const int m0 = __builtin_amdgcn_readfirstlane(blk.m0);
     const int m1 = __builtin_amdgcn_readfirstlane(blk.m1);
