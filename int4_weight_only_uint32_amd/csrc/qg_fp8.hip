@@ -17,8 +17,8 @@ namespace {
 
 constexpr int KB8 = 128;   // k extent of a scale block, bytes of a tile row
 
-// An offset past every buffer range here (at most 2^32 - 2^23 bytes, which the
-// caller checks), also after a step's scalar offset (below 2^22 + 256) is added.
+// An offset past every buffer range here (a block's rows, or with a row index all
+// of A: at most 2^32 - 2^23 bytes, which the caller checks), also after a step's scalar offset (below 2^22 + 256) is added.
 constexpr unsigned FP8_PAST = 0xFFBFFFF0u - 0x1000u;
 // The same for a tile of W: at most 256 rows, 2^30 bytes, and scalar offsets
 // up to such a tile.
@@ -176,11 +176,11 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void fp8_tiled_kernel(
     // every lane's source chunk within a row, and its rows' byte offsets; rows
     // past the end read the last row (never stored)
     const int chunk = (lane & 7) ^ (lane >> 3);
-    const int rows_n = N - n0 < BN ? N - n0 : BN;
+    const int rows_n = N - n0 < BN ? N - n0 : BN, rows_m = m1 - m0 < BM ? m1 - m0 : BM;
     const uint8_t *W = Wall + ((size_t)e * N + n0) * K;
     const __amdgpu_buffer_rsrc_t w_rs = buffer_rsrc(W, (size_t)rows_n * K);
     const __amdgpu_buffer_rsrc_t a_rs =
-        a_rows ? buffer_rsrc(Aall, (size_t)M_a * K) : buffer_rsrc(Aall + (size_t)m0 * K, (size_t)(m1 - m0) * K);
+        a_rows ? buffer_rsrc(Aall, (size_t)M_a * K) : buffer_rsrc(Aall + (size_t)m0 * K, (size_t)rows_m * K);
     unsigned a_off[LA];
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void fp8_tiled_kernel(
     __syncthreads();
     const int my_row = wm * MT * 16 + (lane & 15);     // of m-tile 0
     const __amdgpu_buffer_rsrc_t sa_rs = a_rows ? buffer_rsrc(a_scale, (size_t)M_a * KB * 4)
-                                                : buffer_rsrc(a_scale + (size_t)m0 * KB, (size_t)(m1 - m0) * KB * 4);
+                                                : buffer_rsrc(a_scale + (size_t)m0 * KB, (size_t)rows_m * KB * 4);
     int nb = (n0 + wn * NT * 16) / 128;
     nb = nb < NB ? nb : NB - 1;
     const __amdgpu_buffer_rsrc_t sw_rs = buffer_rsrc(Sall + ((size_t)e * NB + nb) * KB, (size_t)KB * 4);
@@ -524,12 +524,12 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
-    const int rows_n = N - n0 < BN ? N - n0 : BN;
+    const int rows_n = N - n0 < BN ? N - n0 : BN, rows_m = m1 - m0 < BM ? m1 - m0 : BM;
     const __amdgpu_buffer_rsrc_t w_rs = buffer_rsrc(Wall + ((size_t)e * N + n0) * K, (size_t)rows_n * K);
     const __amdgpu_buffer_rsrc_t a_rs =
-        a_rows ? buffer_rsrc(Aall, (size_t)M_a * K) : buffer_rsrc(Aall + (size_t)m0 * K, (size_t)(m1 - m0) * K);
+        a_rows ? buffer_rsrc(Aall, (size_t)M_a * K) : buffer_rsrc(Aall + (size_t)m0 * K, (size_t)rows_m * K);
     const __amdgpu_buffer_rsrc_t sa_rs = a_rows ? buffer_rsrc(a_scale, (size_t)M_a * KB * 4)
-                                                : buffer_rsrc(a_scale + (size_t)m0 * KB, (size_t)(m1 - m0) * KB * 4);
+                                                : buffer_rsrc(a_scale + (size_t)m0 * KB, (size_t)rows_m * KB * 4);
     const __amdgpu_buffer_rsrc_t sw_rs = buffer_rsrc(Sall + ((size_t)e * NB + n0 / 128) * KB, (size_t)KB * 4);
 
     // row of A that row i of the block takes (the last row again past the end),
@@ -755,13 +755,13 @@ hipError_t tiled(const Fp8Args &a, int col_first, int col_end, hipStream_t st)
 
 // Column blocks of 256 for the large tile, the rest for the 128 x 128 one: whole
 // rounds of the chip's 256 CUs, where what is left over would be less than half
-// a round (4096 x 17408 x 5120: 4.25 rounds).  All of them where the counts are
-// not the host's.
+// a round (4096 x 17408 x 5120: 4.25 rounds, 345 against 355 us).  All of them where
+// the counts are not the host's, and where a column block is a large part of a round.
 int large_cols(const Fp8Args &a)
 {
     const int rbs = (a.M + 255) / 256, nbn = (a.N + 255) / 256;
     const long long tiles = (long long)rbs * nbn, over = tiles % 256;
-    if (a.offsets || tiles < 256 || over == 0 || over > 112) return nbn;
+    if (a.offsets || tiles < 256 || rbs > 64 || over == 0 || over > 112) return nbn;
     return (int)((tiles - over) / rbs);
 }
 

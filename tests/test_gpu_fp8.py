@@ -377,6 +377,20 @@ def test_outputs_and_rows_past_32_bit_offsets():
     for r in (0, 65535, 131000):
         check(C[r:r + 73], *dequant(a[r:r + 73], sa[r:r + 73], w, sw), torch.float16)
     del C
+    # 4.4e9 bytes of codes with a partial last k block: what lies behind it reads as
+    # zeros for the first rows too
+    M, K = 1060000, 4112
+    a = torch.zeros((M, K), dtype=torch.uint8, device="cuda")
+    a.view(-1)[2**32 - 2**23:] = 0x7F                # (NaN codes where a far offset could land)
+    part = codes((300, K), 11)
+    a[:300] = part.view(torch.uint8)
+    a[-300:] = part.view(torch.uint8)
+    sa, w, sw = torch.full((M, kb(K)), 0.25, device="cuda"), codes((16, K), 12), scales((1, kb(K)), 13)
+    C = qg.fp8_gemm(a.view(F8), sa, w, sw)
+    torch.cuda.synchronize()
+    for r in (slice(0, 300), slice(M - 300, M)):
+        check(C[r], *dequant(part, sa[:300], w, sw), torch.bfloat16)
+    del a, sa, C
     Ma, K = 2**20, 4080
     a = torch.zeros((Ma, K), dtype=torch.uint8, device="cuda").view(F8)
     a[-9:] = codes((9, K), 7)
