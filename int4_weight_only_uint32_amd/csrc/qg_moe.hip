@@ -482,9 +482,9 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
 // bits, so a slot's rank is a count of lower lanes and no order of atomics
 // decides anything.  Few slots: one workgroup, one launch.  More: one launch
 // counts each workgroup's slots per expert, the next adds the counts of the
-// workgroups before it (each for itself: 64 rows of E counts out of L2).
+// workgroups before it (each for itself, up to 256 rows of E counts).
 constexpr int SORT_MAX_E = 1024, SORT_WAVES = 8, SORT_THREADS = 64 * SORT_WAVES;
-constexpr int SORT_ONE = 4096;       // slots up to which one workgroup does it all
+constexpr int SORT_ONE = 2048;       // slots up to which one workgroup does it all (4000: 8.3 us, with two launches 7.5)
 constexpr int SORT_MAX_WGS = 256;
 
 // Per-wave counts of this workgroup's slots [s0, s1), run slots to a wave.
@@ -539,9 +539,11 @@ __device__ inline void sort_place(const int32_t *__restrict__ ids, int s0, int s
     const int a = s0 + wave * run, b = a + run < s1 ? a + run : s1;
     const unsigned long long below = (1ull << lane) - 1;
     volatile int *next = cnt[wave];
+    int ahead = a + lane < b ? ids[a + lane] : -1;
     for (int sb = a; sb < b; sb += 64) {
         const int s = sb + lane;
-        const int raw = s < b ? ids[s] : -1;
+        const int raw = ahead;
+        ahead = s + 64 < b ? ids[s + 64] : -1;
         const int id = raw >= 0 && raw < E ? raw : E;
         unsigned long long same = ~0ull;
         for (int k = 0; k < bits; ++k) {
@@ -620,16 +622,30 @@ __global__ __launch_bounds__(SORT_THREADS) void moe_sort_place_kernel(
     const int tid = threadIdx.x, wgs = gridDim.x, me = blockIdx.x;
     const int s0 = me * (run * SORT_WAVES);
     const int s1 = n - s0 < run * SORT_WAVES ? n : s0 + run * SORT_WAVES;
-    for (int e = tid; e < E; e += SORT_THREADS) {
+    for (int e = tid; e < E; e += SORT_THREADS) tot[e] = before[e] = 0;
+    __syncthreads();
+    // The counts of all workgroups: the threads that E leaves over share the rows, and
+    // each thread's loads are in flight together (they come from other XCDs)
+    const int span = E > SORT_THREADS / 2 ? SORT_THREADS : E > 1 ? 1 << (32 - __builtin_clz(E - 1)) : 1;
+    const int parts = SORT_THREADS / span, part = tid / span;
+    for (int e = tid - part * span; e < E; e += span) {
         int all = 0, mine = 0;
-#pragma unroll 16
-        for (int w = 0; w < wgs; ++w) {
-            const int c = hist[(size_t)w * E + e];
-            all += c;
-            mine += w < me ? c : 0;
+        for (int w0 = part; w0 < wgs; w0 += 32 * parts) {
+            int c[32];
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+                const int w = w0 + u * parts;      // (past the end: the last row again, not counted)
+                c[u] = hist[(unsigned)(w < wgs ? w : wgs - 1) * E + e];
+            }
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+                const int w = w0 + u * parts;
+                all += w < wgs ? c[u] : 0;
+                mine += w < me ? c[u] : 0;
+            }
         }
-        tot[e] = all;
-        before[e] = mine;
+        atomicAdd(&tot[e], all);
+        atomicAdd(&before[e], mine);
     }
     sort_count(ids, s0, s1, run, E, cnt);      // (its barriers publish tot and before)
     sort_scan(sums, E, tot, first);
@@ -751,13 +767,14 @@ hipError_t launch_moe_route(const void *logits, int dtype, const float *bias, in
 }
 
 namespace {
-// Slots of one wave (a multiple of 64): 2048 slots to a workgroup until 256
-// workgroups would not do, one workgroup for few.
+// Slots of one wave (a multiple of 64): 1024 slots to a workgroup until 256
+// workgroups would not do, one workgroup for few.  16383 x 8 slots of 256 experts:
+// 10.6 us (2048 a workgroup: 10.9, 512: 13.1), 2000 x 8 of 128: 8.2 (9.8, 7.3).
 int sort_run(long long n)
 {
     if (n <= SORT_ONE) return (int)((n + SORT_THREADS - 1) / SORT_THREADS * 64);
     const long long per = (n + (long long)SORT_MAX_WGS * SORT_THREADS - 1) / ((long long)SORT_MAX_WGS * SORT_THREADS) * 64;
-    return (int)(per < 256 ? 256 : per);
+    return (int)(per < 128 ? 128 : per);
 }
 int sort_wgs(long long n)
 {
