@@ -15,6 +15,7 @@ w4a16_swiglu, correct, quantize_rows, w4a8, quantize_fp8, fp8_gemm, route,
 sort_rows and combine_rows are the same calls with torch-allocated outputs.
 """
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -418,35 +419,36 @@ def _dtype(t: torch.Tensor, name: str, f32=False) -> int:
     return code
 
 
-def _arg(t: Optional[torch.Tensor], dtype, shape, device, name):
-    """The pointer of a contiguous device tensor of this type, shape and device."""
+def _arg(t: Optional[torch.Tensor], dtype, shape, dev, name):
+    """The pointer of a contiguous tensor of this type and shape on GPU `dev`
+    (an index, -1 for none)."""
     if t is None:
         return None
-    if (isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype is dtype) and t.shape == shape and
-            t.device == device and t.is_contiguous()):
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev >= 0 and (dtype is None or t.dtype is dtype) and
+            t.shape == shape and t.is_contiguous()):
         return t.data_ptr()
     _ptr(t, dtype, name)         # says what is wrong, if it is one of its checks
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} is on {t.device}, not on {device}")
+    raise ValueError(f"{name} is on {t.device}, not on GPU {dev}")
 
 
-def _raw_stream(index: int) -> int:
-    """The handle of a device's current stream, without a Stream object where
-    torch offers that (1.8 us less of a 7 us call)."""
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+# The handle of a device's current stream and the current device's index without
+# the objects that torch.cuda makes of them (2 us of a 7 us call), where torch
+# has these.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _call(fn, device, *args):
-    """fn(*args, stream) on `device`'s current stream; the library launches on
+def _call(fn, dev, *args):
+    """fn(*args, stream) on GPU `dev`'s current stream; the library launches on
     the current device, so another one is made current for the call."""
-    st = _raw_stream(device.index)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, st)
+    if dev == _current_device():
+        rc = fn(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, st)
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev))
     if rc != QG_OK:
         _check(rc)
 
@@ -460,7 +462,7 @@ def quantize_rows_fp8(A, M, K, flags, A_q, a_scale):
     [M,2K]) fp16 or bf16, A_q float8_e4m3fn, a_scale fp32."""
     d = _dtype(A, "A")
     pair = 2 if flags & QG_QUANT_SWIGLU else 1
-    dev = A.device
+    dev = A.get_device()
     _call(lib().quantize_rows_fp8, dev, _arg(A, None, (M, pair * K), dev, "A"), d, M, K, flags,
           _arg(A_q, torch.float8_e4m3fn, (M, K), dev, "A_q"),
           _arg(a_scale, torch.float32, (M, _blocks128(K)), dev, "a_scale"))
@@ -489,7 +491,7 @@ def qgemm_fp8(A_q, a_scale, a_rows, M_a, W, w_scale, expert_offsets, num_experts
     """Same arguments as the C entry point (dtype is C's); W [E,N,K] (or [N,K]
     with one expert) float8_e4m3fn, w_scale [E, ceil(N/128), ceil(K/128)]."""
     d = _dtype(C, "C")
-    dev, E, KB, NB = A_q.device, num_experts, _blocks128(K), _blocks128(N)
+    dev, E, KB, NB = A_q.get_device(), num_experts, _blocks128(K), _blocks128(N)
     one = W.dim() == 2
     if one and E != 1:
         raise ValueError(f"W holds one expert, not {E}")
@@ -521,7 +523,7 @@ def fp8_gemm(A_q: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor, w_scale:
 def moe_route(logits, bias, T, E, topk, n_group, topk_group, scaling, flags, ids, weights):
     """Same arguments as the C entry point (dtype is the logits')."""
     d = _dtype(logits, "logits", f32=True)
-    dev = logits.device
+    dev = logits.get_device()
     _call(lib().moe_route, dev, _arg(logits, None, (T, E), dev, "logits"), d,
           _arg(bias, torch.float32, (E,), dev, "bias"), T, E, topk, n_group, topk_group, scaling, flags,
           _arg(ids, torch.int32, (T, topk), dev, "ids"),
@@ -552,12 +554,17 @@ def route(logits: torch.Tensor, topk: int, bias: Optional[torch.Tensor] = None, 
 
 def moe_sort_rows(ids, T, topk, num_experts, expert_offsets, row_token, slot_row, workspace=None):
     """Same arguments as the C entry point."""
-    dev = ids.device
+    dev = ids.get_device()
     _call(lib().moe_sort_rows, dev, _arg(ids, torch.int32, (T, topk), dev, "ids"), T, topk, num_experts,
           _arg(expert_offsets, torch.int32, (num_experts + 1,), dev, "expert_offsets"),
           _arg(row_token, torch.int32, (T * topk,), dev, "row_token"),
           _arg(slot_row, torch.int32, (T, topk), dev, "slot_row"), _ptr(workspace, None, "workspace"),
           0 if workspace is None else workspace.numel() * workspace.element_size())
+
+
+@functools.lru_cache(maxsize=1024)
+def _sort_workspace(T, topk, num_experts):
+    return qg_workspace_bytes(QG_OP_MOE_SORT, T, topk, 0, 0, num_experts, 0)
 
 
 def sort_rows(ids: torch.Tensor, num_experts: int, expert_offsets: Optional[torch.Tensor] = None,
@@ -572,7 +579,7 @@ def sort_rows(ids: torch.Tensor, num_experts: int, expert_offsets: Optional[torc
         row_token = torch.empty((T * topk,), dtype=torch.int32, device=ids.device)
     if slot_row is None:
         slot_row = torch.empty((T, topk), dtype=torch.int32, device=ids.device)
-    n = qg_workspace_bytes(QG_OP_MOE_SORT, T, topk, 0, 0, num_experts, 0)
+    n = _sort_workspace(T, topk, num_experts)
     # from torch's allocator on each call: nothing is kept in it, and calls on
     # other streams or in graphs captured side by side get their own
     ws = torch.empty(n, dtype=torch.uint8, device=ids.device) if n > 0 else None
@@ -583,7 +590,7 @@ def sort_rows(ids: torch.Tensor, num_experts: int, expert_offsets: Optional[torc
 def moe_combine_rows(Y, slot_row, weights, T, topk, M_rows, N, out):
     """Same arguments as the C entry point (dtype is Y's)."""
     d = _dtype(Y, "Y")
-    dev = Y.device
+    dev = Y.get_device()
     _call(lib().moe_combine_rows, dev, _arg(Y, None, (M_rows, N), dev, "Y"), d,
           _arg(slot_row, torch.int32, (T, topk), dev, "slot_row"),
           _arg(weights, torch.float32, (T, topk), dev, "weights"), T, topk, M_rows, N,
