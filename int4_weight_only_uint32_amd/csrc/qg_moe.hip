@@ -154,10 +154,21 @@ __device__ inline void route_exact(const RouteArgs &a, int t, double *sh)
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         double v = NINF, v2 = NINF;
         if (lane < a.n_group) {
-            for (int j = 0; j < size; ++j) {
+            int j = 0;
+            for (; j + 8 <= size; j += 8) {      // eight reads in flight
+                double x[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) x[u] = sh[lane * size + j + u];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    v2 = __builtin_fmax(v2, __builtin_fmin(v, x[u]));
+                    v = __builtin_fmax(v, x[u]);
+                }
+            }
+            for (; j < size; ++j) {
                 const double x = sh[lane * size + j];
-                if (x > v) { v2 = v; v = x; }
-                else if (x > v2) v2 = x;
+                v2 = __builtin_fmax(v2, __builtin_fmin(v, x));
+                v = __builtin_fmax(v, x);
             }
         }
         if (sums && v2 != NINF) v += v2;
@@ -173,36 +184,42 @@ __device__ inline void route_exact(const RouteArgs &a, int t, double *sh)
             if (e < a.E && !((keep >> (e / size)) & 1)) choice[i] = NINF;
         }
     }
+    // keys of the same order as the choices (0 for a masked expert); the largest of
+    // the wave by its upper words, then by the lower ones of those that have it
+    unsigned long long key[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const unsigned long long b = __builtin_bit_cast(unsigned long long, choice[i] + 0.0);
+        key[i] = choice[i] == NINF ? 0ull : (b >> 63) ? ~b : b | (1ull << 63);
+    }
     double mine = 0;
     int my_id = -1;
     for (int j = 0; j < a.topk; ++j) {
-        double best = NINF, s = 0;
-        int id = 0x7fffffff;
+        unsigned long long best = 0;
+        double s = 0;
+        int id = 0;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            if (choice[i] > best) {
-                best = choice[i];
+            if (key[i] > best) {
+                best = key[i];
                 s = score[i];
                 id = lane * VPL + i;
             }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            const double ob = __shfl_xor(best, o), os = __shfl_xor(s, o);
-            const int oi = __shfl_xor(id, o);
-            if (ob > best || (ob == best && oi < id)) {
-                best = ob;
-                s = os;
-                id = oi;
-            }
-        }
-        if (best == NINF) break;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (lane * VPL + i == id) choice[i] = NINF;
+        const unsigned hi = wave_max((unsigned)(best >> 32));
+        if (hi == 0) break;
+        const bool has = (unsigned)(best >> 32) == hi;
+        const unsigned lo = wave_max(has ? (unsigned)best : 0u);
+        const int owner = __builtin_ctzll(__ballot(has && (unsigned)best == lo));
+        const long long sb = __builtin_bit_cast(long long, s);
+        const unsigned s_lo = (unsigned)__builtin_amdgcn_readlane((int)sb, owner);
+        const unsigned s_hi = (unsigned)__builtin_amdgcn_readlane((int)(sb >> 32), owner);
+        id = __builtin_amdgcn_readlane(id, owner);
         if (lane == j) {
-            mine = s;
+            mine = __builtin_bit_cast(double, (unsigned long long)s_hi << 32 | s_lo);
             my_id = id;
         }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) key[i] = lane * VPL + i == id ? 0ull : key[i];
     }
     double sum = mine;
 #pragma unroll
