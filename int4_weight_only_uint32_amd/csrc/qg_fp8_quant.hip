@@ -43,13 +43,13 @@ __device__ inline void widen8(const uint4v &a, float (&x)[8])
     }
 }
 
-// silu(g) * u in binary32, within 2^-21 of its size.  Below -88 silu is 0 to
-// 2e-37 |g|; infinities and NaN give a NaN or an infinity.
-__device__ inline float silu_near(float g, float u)
+// silu(g) in binary32 within 2^-22 of its size for g > -87; below, a value of
+// less than SILU_SMALL (a NaN or infinity gives a NaN or an infinity).
+constexpr float SILU_SMALL = 0x1p-100f;
+__device__ inline float silu_near(float g)
 {
-    const float x = __builtin_fminf(__builtin_fmaxf(-g, -87.0f), 88.0f);
-    const float s = rcp_near(1.0f + exp_near(x));
-    return g * (g > -88.0f ? s : 0.0f) * u;
+    const float x = __builtin_fminf(__builtin_fmaxf(-g, -87.0f), 87.0f);
+    return g * rcp_near(1.0f + exp_near(x));
 }
 
 __device__ inline double silu_64(float g, float u)
@@ -86,8 +86,36 @@ __global__ __launch_bounds__(256) void quantize_rows_fp8_kernel(
     widen8<BF16>(g, x);
     if (SWIGLU) {
         widen8<BF16>(u, y);
+        float least = __builtin_inff();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = silu_near(x[j], y[j]);
+        for (int j = 0; j < 8; ++j) {
+            const float s = silu_near(x[j]);
+            least = __builtin_fminf(least, __builtin_fabsf(s));
+            x[j] = s * y[j];
+        }
+        if (least < SILU_SMALL) {
+            // A bf16 up value may raise a silu near or below binary32's least values
+            // back to any size: those in 64 bits.
+            float xg[8];
+            widen8<BF16>(g, xg);
+            unsigned redo = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                redo |= (xg[j] < -60.0f || (__builtin_fabsf(xg[j]) < 2 * SILU_SMALL && xg[j] != 0.0f) ? 1u : 0u) << j;
+            while (redo) {
+                const int at_j = __builtin_ctz(redo);
+                float gj = 0.f, uj = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    gj = j == at_j ? xg[j] : gj;
+                    uj = j == at_j ? y[j] : uj;
+                }
+                const float v = (float)silu_64(gj, uj);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = j == at_j ? v : x[j];
+                redo &= redo - 1;
+            }
+        }
     }
     // magnitudes as bit patterns: ordered as the values are, NaN above infinity
     unsigned mx = 0;
@@ -103,8 +131,9 @@ __global__ __launch_bounds__(256) void quantize_rows_fp8_kernel(
     if (mx >= 0x7f800000u) {
         sc = __builtin_nanf("");
     } else if (SWIGLU) {
-        // the values that may be the largest: those within 2^-19 of it
-        const float near = __builtin_bit_cast(float, mx) * (1.0f - 0x1p-19f);
+        // the values that may be the largest: those within 2^-19 of it; all where
+        // binary32 holds them with fewer bits
+        const float big = __builtin_bit_cast(float, mx), near = big < 0x1p-100f ? 0.f : big * (1.0f - 0x1p-19f);
         unsigned cand = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) cand |= (__builtin_fabsf(x[j]) >= near && mx ? 1u : 0u) << j;

@@ -148,6 +148,40 @@ def test_quantize_swiglu_non_finite_and_far_gates():
         assert torch.equal(q[r, 128 * c:128 * c + 128], rq[r, 128 * c:128 * c + 128]), (r, c)
 
 
+@pytest.mark.parametrize("far", [-60.0, -86.5, -87.5, -88.5, -95.0, -120.0, 1e-37, -1e-37, 9e-40])
+def test_quantize_swiglu_gates_that_only_the_product_raises(far):
+    """silu(gate) near or under the least 32-bit value, times a bf16 up value as
+    large as the type's: an ordinary product.  In every position of a block, as
+    its only value, among ordinary ones, and with a small up value (a product that
+    32 bits hold with few bits or not at all)."""
+    far = float(torch.tensor(far).bfloat16())
+    K, n = 128, 24
+    gate, up = torch.zeros(6 * n, K), torch.zeros(6 * n, K)
+    g = torch.Generator().manual_seed(int(abs(far) * 8) + 1)
+    silu = abs(far / (1.0 + np.exp(-far)))
+    for i in range(n):
+        at = (5 * i) % K
+        gate[6 * i:6 * i + 6, at] = far
+        gate[6 * i + 1], up[6 * i + 1] = torch.randn(2, K, generator=g)
+        gate[6 * i + 1, at] = far
+        gate[6 * i + 4] = far
+        gate[6 * i + 5] = far
+        most = 1e38 * (i + 1) / n * 3
+        up[6 * i, at] = most
+        up[6 * i + 1, at] = min(most, (i + 1) / 8.0 / silu)    # about as large as the others
+        up[6 * i + 2, at] = 1e-3 * (i + 1)
+        up[6 * i + 3, at] = min(most, 2.0 ** (-150 + i) / silu)
+        up[6 * i + 4] = torch.randn(K, generator=g) * min(1e37, 1e3 / silu)
+        up[6 * i + 5] = torch.randn(K, generator=g) * min(1e37, 1e-41 / silu)
+    x = torch.cat([gate, up], 1).bfloat16()
+    q, s = qg.quantize_fp8(x.cuda(), swiglu=True)
+    torch.cuda.synchronize()
+    gate, up = x.double().chunk(2, 1)
+    rq, rs = ref_quant(gate / (1.0 + torch.exp(-gate)) * up)
+    assert torch.equal(s.cpu(), rs)
+    assert torch.equal(q.cpu().double(), rq)
+
+
 def codes(shape, seed, scale=1.0):
     """Random codes (on the GPU) and their values."""
     g = torch.Generator(device="cuda").manual_seed(seed)
