@@ -78,7 +78,7 @@ __device__ inline float key_value(unsigned k)
 
 __device__ inline float sigmoid_near(float l)
 {
-    // (clamped: below, the result is under 2^-126 and the caller's sums tell)
+    // (clamped: beyond, the result is under 2^-120, and weights like that are taken in 64 bits)
     const float x = __builtin_fminf(__builtin_fmaxf(-l, -87.0f), 87.0f);
     return rcp_near(1.0f + exp_near(x));
 }
@@ -479,8 +479,8 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
         s = sigmoid ? sigmoid_near(x) : exp_of(x) * inv;
     }
     const float sum = wave_sum(s);
-    // scores that run out of 32 bits: in 64
-    if (renorm && sum < 0x1p-60f && __ballot(my_id >= 0)) unsure = true;
+    // weights that run out of 32 bits: in 64
+    if (__ballot(my_id >= 0 && s < 0x1p-120f)) unsure = true;
     if (unsure) {
         route_exact<VPL>(a, t, sh[wave]);
         return;

@@ -118,6 +118,24 @@ def test_route_many_tokens():
     assert float((w.double() - 2.5 * rw / rw.sum(1, keepdim=True)).abs().max()) <= 40 * 2.0**-24 * 2.5
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_route_weights_down_to_the_least_values(score, renormalize):
+    """Scores down to 2^-149 and below, with and without a largest one beside
+    them: each weight to its own size.  (fast path: as check_route; the 64-bit one
+    rounds once; both to half the least step, 2^-150, times the scaling.)"""
+    x = torch.linspace(-110, -60, 64).repeat(8, 1)
+    for t in range(8):
+        x[t] = x[t, torch.randperm(64, generator=torch.Generator().manual_seed(t))] + t / 8
+    x[1::2, 7] = 3.0
+    ids, w = qg.route(x.cuda(), 64, score=score, renormalize=renormalize, scaling=2.5)
+    torch.cuda.synchronize()
+    ri, rw = ref_route(x, 64, score=score, renormalize=renormalize, scaling=2.5)
+    assert (ids.cpu().numpy() == ri).all()
+    tol = (113 + 16) * 2.0**-24 * np.abs(rw) + 2.5 * 2.0**-150
+    assert (np.abs(w.cpu().double().numpy() - rw) <= tol).all()
+
+
 def test_route_scores_closer_than_32_bits():
     """Choices that differ by less than a 32-bit step, in every position: the
     order is that of the real numbers."""
