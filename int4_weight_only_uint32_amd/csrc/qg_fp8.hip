@@ -73,43 +73,64 @@ __device__ inline int row_block_count(const int32_t *__restrict__ offsets, int E
     return n;
 }
 
-// Row block rb; {0, 0, 0} if there are fewer.  first: scan_rows from expert 0 on.
-__device__ inline RowBlock find_rows(const int32_t *__restrict__ offsets, int E, int M, int BM,
-                                     int rb, const RowScan &first)
+// Row block rb, or the expert it belongs to (m0 its first row, `before` the
+// row blocks of the experts before it, `blocks` its own); no rows if there are fewer.
+// first: scan_rows from expert 0 on.
+struct ExpertRows {
+    int e, m0, m1, before, blocks;
+};
+__device__ inline ExpertRows find_expert(const int32_t *__restrict__ offsets, int E, int M, int BM,
+                                         int rb, const RowScan &first)
 {
-    if (!offsets) return RowBlock{0, rb * BM, M};
+    if (!offsets) return ExpertRows{0, 0, M, 0, (M + BM - 1) / BM};
     RowScan s = first;
     int base = 0;
     for (int e0 = 0;;) {
         const unsigned long long hit = __ballot(base + s.sum > rb);
         if (hit) {
             const int l = __builtin_ctzll(hit);
-            const int before = base + __builtin_amdgcn_readlane(s.sum - s.blocks, l);
-            return RowBlock{e0 + l, __builtin_amdgcn_readlane(s.r0, l) + (rb - before) * BM,
-                            __builtin_amdgcn_readlane(s.r1, l)};
+            return ExpertRows{e0 + l, __builtin_amdgcn_readlane(s.r0, l), __builtin_amdgcn_readlane(s.r1, l),
+                              base + __builtin_amdgcn_readlane(s.sum - s.blocks, l),
+                              __builtin_amdgcn_readlane(s.blocks, l)};
         }
         base += __builtin_amdgcn_readlane(s.sum, 63);
         e0 += 64;
-        if (e0 >= E) return RowBlock{0, 0, 0};
+        if (e0 >= E) return ExpertRows{0, 0, 0, 0, 0};
         s = scan_rows(offsets, E, M, BM, e0);
     }
+}
+__device__ inline RowBlock find_rows(const int32_t *__restrict__ offsets, int E, int M, int BM,
+                                     int rb, const RowScan &first)
+{
+    const ExpertRows x = find_expert(offsets, E, M, BM, rb, first);
+    if ((unsigned)(rb - x.before) >= (unsigned)x.blocks) return RowBlock{0, 0, 0};
+    return RowBlock{x.e, x.m0 + (rb - x.before) * BM, x.m1};
 }
 
 // The tile of workgroup b out of rbs row blocks x nbn column blocks, false if
 // there is none.  Workgroups go to the eight XCDs in turn; each XCD takes a
-// contiguous run of the tiles, ordered in bands of GM row blocks, so that the
-// tiles an XCD computes at a time share both operands in its L2.
-template <int GM>
-__device__ inline bool tile_of(int b, int rbs, int nbn, int &rb, int &nb)
+// contiguous run of the tiles, ordered expert by expert and in bands of 1536 of an
+// expert's rows, so that the tiles an XCD computes at a time share both operands in
+// its L2.  4096 tokens to 8 of 64 experts at 2048 x 7168: 610 us (bands of 1024
+// rows 621; bands that run over the experts' borders 647), dense no difference.
+template <int BM>
+__device__ inline bool tile_of(int b, const int32_t *__restrict__ offsets, int E, int M, int nbn,
+                               RowBlock &blk, int &nb)
 {
-    const int tiles = rbs * nbn;
+    constexpr int GM = 1536 / BM;
+    RowScan scan = {};
+    if (offsets) scan = scan_rows(offsets, E, M, BM, 0);
+    const int tiles = row_block_count(offsets, E, M, BM, scan) * nbn;
     if (b >= tiles) return false;
     const int x = b & 7, q = tiles >> 3, r = tiles & 7;
     const int id = x * q + (x < r ? x : r) + (b >> 3);
-    const int band = id / (GM * nbn), in = id - band * (GM * nbn);
-    const int rows = rbs - band * GM < GM ? rbs - band * GM : GM;
-    nb = in / rows;
-    rb = band * GM + in - nb * rows;
+    const ExpertRows rows = find_expert(offsets, E, M, BM, id / nbn, scan);
+    const int of = id - rows.before * nbn;
+    if ((unsigned)of >= (unsigned)(rows.blocks * nbn)) return false;      // (offsets that are none)
+    const int band = of / (GM * nbn), in = of - band * (GM * nbn);
+    const int high = rows.blocks - band * GM < GM ? rows.blocks - band * GM : GM;
+    nb = in / high;
+    blk = RowBlock{rows.e, rows.m0 + (band * GM + in - nb * high) * BM, rows.m1};
     return true;
 }
 
@@ -155,13 +176,11 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void fp8_tiled_kernel(
     extern __shared__ __attribute__((aligned(16))) uint8_t lds_all[];
     constexpr int STAGE = (BM + BN) * KB8;
 
-    int rb, n0;
+    int n0;
+    RowBlock blk;
     // uniform over the workgroup, before any barrier
-    RowScan scan = {};
-    if (offsets) scan = scan_rows(offsets, E, M, BM, 0);
-    if (!tile_of<1024 / BM>(blockIdx.x, row_block_count(offsets, E, M, BM, scan), nbn, rb, n0)) return;
+    if (!tile_of<BM>(blockIdx.x, offsets, E, M, nbn, blk, n0)) return;
     n0 = col_first + n0 * BN;
-    const RowBlock blk = find_rows(offsets, E, M, BM, rb, scan);
     const int e = __builtin_amdgcn_readfirstlane(blk.e);
     const int m0 = __builtin_amdgcn_readfirstlane(blk.m0);
     const int m1 = __builtin_amdgcn_readfirstlane(blk.m1);
