@@ -407,7 +407,8 @@ def w4a16_swiglu(A: torch.Tensor, pair: PackedWeight, H: Optional[torch.Tensor] 
 
 
 # The calls below check shapes exactly and run on the current stream of their
-# first tensor's device, whichever device is current.
+# first tensor's device, whichever device is current.  Forward only: their
+# results carry no gradient.
 
 _DTYPES = {torch.float16: QG_DTYPE_F16, torch.bfloat16: QG_DTYPE_BF16, torch.float32: QG_DTYPE_F32}
 
@@ -457,10 +458,17 @@ def _blocks128(n: int) -> int:
     return -(-n // 128)
 
 
+def _too_many(*counts):
+    """The C entry points count in 32 bits; ctypes would cut a larger number."""
+    raise ValueError(f"counts {counts} must lie in 0 .. 2^31 - 1")
+
+
 def quantize_rows_fp8(A, M, K, flags, A_q, a_scale):
     """Same arguments as the C entry point; A [M,K] (or, QG_QUANT_SWIGLU,
     [M,2K]) fp16 or bf16, A_q float8_e4m3fn, a_scale fp32."""
     d = _dtype(A, "A")
+    if (M | K) >> 31:
+        _too_many(M, K)
     pair = 2 if flags & QG_QUANT_SWIGLU else 1
     dev = A.get_device()
     _call(lib().quantize_rows_fp8, dev, _arg(A, None, (M, pair * K), dev, "A"), d, M, K, flags,
@@ -491,6 +499,8 @@ def qgemm_fp8(A_q, a_scale, a_rows, M_a, W, w_scale, expert_offsets, num_experts
     """Same arguments as the C entry point (dtype is C's); W [E,N,K] (or [N,K]
     with one expert) float8_e4m3fn, w_scale [E, ceil(N/128), ceil(K/128)]."""
     d = _dtype(C, "C")
+    if (M_a | M_total | num_experts | N | K) >> 31:
+        _too_many(M_a, M_total, num_experts, N, K)
     dev, E, KB, NB = A_q.get_device(), num_experts, _blocks128(K), _blocks128(N)
     one = W.dim() == 2
     if one and E != 1:
@@ -523,6 +533,8 @@ def fp8_gemm(A_q: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor, w_scale:
 def moe_route(logits, bias, T, E, topk, n_group, topk_group, scaling, flags, ids, weights):
     """Same arguments as the C entry point (dtype is the logits')."""
     d = _dtype(logits, "logits", f32=True)
+    if (T | E | topk) >> 31:
+        _too_many(T, E, topk)
     dev = logits.get_device()
     _call(lib().moe_route, dev, _arg(logits, None, (T, E), dev, "logits"), d,
           _arg(bias, torch.float32, (E,), dev, "bias"), T, E, topk, n_group, topk_group, scaling, flags,
@@ -554,6 +566,8 @@ def route(logits: torch.Tensor, topk: int, bias: Optional[torch.Tensor] = None, 
 
 def moe_sort_rows(ids, T, topk, num_experts, expert_offsets, row_token, slot_row, workspace=None):
     """Same arguments as the C entry point."""
+    if (T | topk | num_experts) >> 31:
+        _too_many(T, topk, num_experts)
     dev = ids.get_device()
     _call(lib().moe_sort_rows, dev, _arg(ids, torch.int32, (T, topk), dev, "ids"), T, topk, num_experts,
           _arg(expert_offsets, torch.int32, (num_experts + 1,), dev, "expert_offsets"),
@@ -590,6 +604,8 @@ def sort_rows(ids: torch.Tensor, num_experts: int, expert_offsets: Optional[torc
 def moe_combine_rows(Y, slot_row, weights, T, topk, M_rows, N, out):
     """Same arguments as the C entry point (dtype is Y's)."""
     d = _dtype(Y, "Y")
+    if (T | topk | M_rows | N) >> 31:
+        _too_many(T, topk, M_rows, N)
     dev = Y.get_device()
     _call(lib().moe_combine_rows, dev, _arg(Y, None, (M_rows, N), dev, "Y"), d,
           _arg(slot_row, torch.int32, (T, topk), dev, "slot_row"),

@@ -150,3 +150,23 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         qg.combine_rows(x, torch.zeros(2, 2, dtype=torch.int32), x)
     with pytest.raises(TypeError):
         qg.fp8_gemm(x, x, x, x, dtype=torch.float32)
+
+
+def test_binding_refuses_counts_past_32_bits():
+    """A count of 2^32 + 2 is not the 2 that an int would make of it."""
+    n = 2**32 + 2
+
+    def t(*shape, dtype=torch.float32):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    f8, i32 = torch.float8_e4m3fn, torch.int32
+    calls = [lambda: qg.quantize_fp8(t(n, 16, dtype=torch.float16)),
+             lambda: qg.fp8_gemm(t(n, 16, dtype=f8), t(n, 1), t(16, 16, dtype=f8), t(1, 1)),
+             lambda: qg.fp8_gemm(t(4, 16, dtype=f8), t(4, 1), t(16, 16, dtype=f8), t(1, 1), a_rows=t(n, dtype=i32)),
+             lambda: qg.route(t(n, 8), 2),
+             lambda: qg.combine_rows(t(n, 8, dtype=torch.float16), t(4, 2, dtype=i32), t(4, 2)),
+             lambda: qg.moe_sort_rows(t(n, 2, dtype=i32), n, 2, 8, t(9, dtype=i32), t(2 * n, dtype=i32),
+                                      t(n, 2, dtype=i32))]
+    for call in calls:
+        with pytest.raises(ValueError, match="counts"):
+            call()
