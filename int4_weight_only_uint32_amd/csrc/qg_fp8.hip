@@ -162,12 +162,13 @@ __device__ inline void store4(uint16_t *c, float4v x, bool zero, int n, int N, b
 // KS > 1: KS such groups of waves, each with LDS of its own, take the steps in
 // turn, and their sums meet in LDS in the order of the groups; for grids that
 // leave CUs idle or K long, where a step's latency is what counts.
+// b: the workgroup's number among those of this tile.
 template <int BM, int BN, int WM, int WN, int KS, bool BF16>
-__global__ __launch_bounds__(64 * WM * WN * KS) void fp8_tiled_kernel(
+__device__ __forceinline__ void fp8_tile(
     const uint8_t *__restrict__ Aall, const float *__restrict__ a_scale,
     const int32_t *__restrict__ a_rows, int M_a, const uint8_t *__restrict__ Wall,
     const float *__restrict__ Sall, const int32_t *__restrict__ offsets, int E, int M, int N,
-    int K, int KB, int NB, int col_first, int nbn, uint16_t *__restrict__ C)
+    int K, int KB, int NB, int col_first, int nbn, uint16_t *__restrict__ C, int b)
 {
     constexpr int NW = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
     constexpr int LA = BM / 8 / NW, LW = BN / 8 / NW;    // 1 KB loads per wave and step
@@ -179,7 +180,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void fp8_tiled_kernel(
     int n0;
     RowBlock blk;
     // uniform over the workgroup, before any barrier
-    if (!tile_of<BM>(blockIdx.x, offsets, E, M, nbn, blk, n0)) return;
+    if (!tile_of<BM>(b, offsets, E, M, nbn, blk, n0)) return;
     n0 = col_first + n0 * BN;
     const int e = __builtin_amdgcn_readfirstlane(blk.e);
     const int m0 = __builtin_amdgcn_readfirstlane(blk.m0);
@@ -501,6 +502,36 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void fp8_tiled_kernel(
     }
 }
 
+template <int BM, int BN, int WM, int WN, int KS, bool BF16>
+__global__ __launch_bounds__(64 * WM * WN * KS) void fp8_tiled_kernel(
+    const uint8_t *__restrict__ Aall, const float *__restrict__ a_scale,
+    const int32_t *__restrict__ a_rows, int M_a, const uint8_t *__restrict__ Wall,
+    const float *__restrict__ Sall, const int32_t *__restrict__ offsets, int E, int M, int N,
+    int K, int KB, int NB, int nbn, uint16_t *__restrict__ C)
+{
+    fp8_tile<BM, BN, WM, WN, KS, BF16>(Aall, a_scale, a_rows, M_a, Wall, Sall, offsets, E, M, N, K, KB, NB, 0, nbn, C,
+                                       blockIdx.x);
+}
+
+// Dense, the first `large` workgroups 256 x 256 tiles of the first nbn column blocks,
+// the others BM x BN tiles of the rest, in one launch: a CU that has done its
+// large tiles begins with a small one (4096 x 17408 x 5120: 349 us, as two launches 353).
+template <int BM, int BN, int WM, int WN, int KS, bool BF16>
+__global__ __launch_bounds__(512) void fp8_two_tiles_kernel(
+    const uint8_t *__restrict__ Aall, const float *__restrict__ a_scale,
+    const int32_t *__restrict__ a_rows, int M_a, const uint8_t *__restrict__ Wall,
+    const float *__restrict__ Sall, int M, int N, int K, int KB, int NB, int nbn, int large,
+    uint16_t *__restrict__ C)
+{
+    static_assert(WM * WN * KS == 8, "as many waves as the large tile");
+    if ((int)blockIdx.x < large)
+        fp8_tile<256, 256, 4, 2, 1, BF16>(Aall, a_scale, a_rows, M_a, Wall, Sall, nullptr, 1, M, N, K, KB, NB, 0, nbn,
+                                          C, blockIdx.x);
+    else
+        fp8_tile<BM, BN, WM, WN, KS, BF16>(Aall, a_scale, a_rows, M_a, Wall, Sall, nullptr, 1, M, N, K, KB, NB,
+                                           nbn * 256, (N - nbn * 256 + BN - 1) / BN, C, blockIdx.x - large);
+}
+
 // ---- streaming kernel, few rows ----
 // For row blocks of 16 MT <= 64 rows the weights are read once.  A workgroup
 // holds NT 16-column tiles; its NW waves take the 128-k steps in turn, each with
@@ -755,33 +786,67 @@ Fp8Kernel choose(bool grouped, int E, int M, int N, int K)
     return T64x128;
 }
 
-// The tiled kernel on columns col_first .. col_end - 1 (col_first a multiple of 128).
+template <int BM, int BN, int WM, int WN, int KS>
+constexpr int tile_lds() { return KS * (2 * (BM + BN) * KB8 + WM * WN * (BM / WM / 16) * 256) + BM * 4; }
+
+hipError_t allow_lds(const void *kern, int bytes)
+{
+    if (bytes <= 65536) return hipSuccess;
+    return hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 template <int BM, int BN, int WM, int WN, int KS, bool BF16>
-hipError_t tiled(const Fp8Args &a, int col_first, int col_end, hipStream_t st)
+hipError_t tiled(const Fp8Args &a, hipStream_t st)
 {
     const auto kern = fp8_tiled_kernel<BM, BN, WM, WN, KS, BF16>;
-    constexpr int bytes = KS * (2 * (BM + BN) * KB8 + WM * WN * (BM / WM / 16) * 256) + BM * 4;
-    if (bytes > 65536) {
-        const hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != hipSuccess) return e;
-    }
-    const int nbn = (col_end - col_first + BN - 1) / BN;
+    constexpr int bytes = tile_lds<BM, BN, WM, WN, KS>();
+    const hipError_t e = allow_lds((const void *)kern, bytes);
+    if (e != hipSuccess) return e;
+    const int nbn = (a.N + BN - 1) / BN;
     const long long wgs = row_blocks(a.offsets != nullptr, a.E, a.M, BM) * nbn;
     hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(64 * WM * WN * KS), bytes, st, a.A, a.a_scale, a.a_rows,
-                       a.M_a, a.W, a.w_scale, a.offsets, a.E, a.M, a.N, a.K, a.KB, a.NB, col_first, nbn, a.C);
+                       a.M_a, a.W, a.w_scale, a.offsets, a.E, a.M, a.N, a.K, a.KB, a.NB, nbn, a.C);
     return hipGetLastError();
 }
 
-// Column blocks of 256 for the large tile, the rest for the 128 x 128 one: whole
-// rounds of the chip's 256 CUs, where what is left over would be less than half
-// a round (4096 x 17408 x 5120: 4.25 rounds, 345 against 355 us).  All of them where
-// the counts are not the host's, and where a column block is a large part of a round.
-int large_cols(const Fp8Args &a)
+// The large tile on the first nbn column blocks, a small one on the rest.
+template <int BM, int BN, int WM, int WN, int KS, bool BF16>
+hipError_t two_tiles(const Fp8Args &a, int nbn, hipStream_t st)
 {
-    const int rbs = (a.M + 255) / 256, nbn = (a.N + 255) / 256;
-    const long long tiles = (long long)rbs * nbn, over = tiles % 256;
-    if (a.offsets || tiles < 256 || rbs > 64 || over == 0 || over > 112) return nbn;
-    return (int)((tiles - over) / rbs);
+    const auto kern = fp8_two_tiles_kernel<BM, BN, WM, WN, KS, BF16>;
+    constexpr int large_lds = tile_lds<256, 256, 4, 2, 1>(), small_lds = tile_lds<BM, BN, WM, WN, KS>();
+    constexpr int bytes = large_lds > small_lds ? large_lds : small_lds;
+    const hipError_t e = allow_lds((const void *)kern, bytes);
+    if (e != hipSuccess) return e;
+    const int large = (a.M + 255) / 256 * nbn;
+    const int small = (a.M + BM - 1) / BM * ((a.N - nbn * 256 + BN - 1) / BN);
+    hipLaunchKernelGGL(kern, dim3(large + small), dim3(512), bytes, st, a.A, a.a_scale, a.a_rows, a.M_a, a.W,
+                       a.w_scale, a.M, a.N, a.K, a.KB, a.NB, nbn, large, a.C);
+    return hipGetLastError();
+}
+
+// The large tile.  Where its grid is some rounds of the chip's 256 CUs and part of one, the
+// column blocks past the whole rounds go to the smallest tile that makes one
+// round of them (the counts must be the host's, so not grouped).  us at M = 2048,
+// K = 4096, by the tiles past a round of large ones:
+//   past     all large   64 x 128   128 x 128   128 x 256
+//     16        108          81          85          97
+//     48        112         101          90         104
+//     88        120         129         120         113
+//    152        126                                 147
+template <bool BF16>
+hipError_t large_tiles(const Fp8Args &a, hipStream_t st)
+{
+    const long long rbs = (a.M + 255) / 256, tiles = rbs * ((a.N + 255) / 256);
+    const int nbn = (int)(tiles / 256 * 256 / rbs);
+    const long long cols = a.N - (long long)nbn * 256;
+    auto small = [&](int bm, int bn) { return ((a.M + bm - 1) / bm) * ((cols + bn - 1) / bn); };
+    if (!a.offsets && nbn > 0 && cols > 0) {
+        if (small(64, 128) <= 256) return two_tiles<64, 128, 2, 2, 2, BF16>(a, nbn, st);
+        if (small(128, 128) <= 256) return two_tiles<128, 128, 2, 2, 2, BF16>(a, nbn, st);
+        if (small(128, 256) <= 256) return two_tiles<128, 256, 2, 4, 1, BF16>(a, nbn, st);
+    }
+    return tiled<256, 256, 4, 2, 1, BF16>(a, st);
 }
 
 template <int MT, int NT, int NW, int P, bool BF16>
@@ -789,10 +854,8 @@ hipError_t stream(const Fp8Args &a, hipStream_t st)
 {
     const auto kern = fp8_stream_kernel<MT, NT, NW, P, BF16>;
     constexpr int bytes = NW * P * (16 * (MT + NT) * KB8 + 512);
-    if (bytes > 65536) {
-        const hipError_t e = hipFuncSetAttribute((const void *)kern, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != hipSuccess) return e;
-    }
+    const hipError_t e = allow_lds((const void *)kern, bytes);
+    if (e != hipSuccess) return e;
     const long long wgs = row_blocks(a.offsets != nullptr, a.E, a.M, 16 * MT) * ((a.N + 16 * NT - 1) / (16 * NT));
     hipLaunchKernelGGL(kern, dim3((unsigned)wgs), dim3(64 * NW), bytes, st, a.A, a.a_scale, a.a_rows, a.M_a, a.W,
                        a.w_scale, a.offsets, a.E, a.M, a.N, a.K, a.KB, a.NB, a.C);
@@ -810,17 +873,12 @@ hipError_t launch(const Fp8Args &a, hipStream_t st)
     case S2x4x2: return stream<2, 4, 2, 2, BF16>(a, st);
     case S4x2x4: return stream<4, 2, 4, 2, BF16>(a, st);
     case S4x4x4: return stream<4, 4, 4, 2, BF16>(a, st);
-    case T64x64K2: return tiled<64, 64, 2, 2, 2, BF16>(a, 0, a.N, st);
-    case T64x128: return tiled<64, 128, 2, 2, 1, BF16>(a, 0, a.N, st);
-    case T64x128K2: return tiled<64, 128, 2, 2, 2, BF16>(a, 0, a.N, st);
-    case T128x128K2: return tiled<128, 128, 2, 2, 2, BF16>(a, 0, a.N, st);
-    case T128x256: return tiled<128, 256, 2, 2, 1, BF16>(a, 0, a.N, st);
-    case T256x256: {
-        const int end = large_cols(a) * 256;
-        if (end >= a.N) return tiled<256, 256, 4, 2, 1, BF16>(a, 0, a.N, st);
-        const hipError_t e = tiled<256, 256, 4, 2, 1, BF16>(a, 0, end, st);
-        return e != hipSuccess ? e : tiled<128, 128, 2, 2, 1, BF16>(a, end, a.N, st);
-    }
+    case T64x64K2: return tiled<64, 64, 2, 2, 2, BF16>(a, st);
+    case T64x128: return tiled<64, 128, 2, 2, 1, BF16>(a, st);
+    case T64x128K2: return tiled<64, 128, 2, 2, 2, BF16>(a, st);
+    case T128x128K2: return tiled<128, 128, 2, 2, 2, BF16>(a, st);
+    case T128x256: return tiled<128, 256, 2, 2, 1, BF16>(a, st);
+    case T256x256: return large_tiles<BF16>(a, st);
     }
     return hipErrorUnknown;
 }

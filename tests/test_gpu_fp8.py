@@ -244,7 +244,9 @@ WIDE = [
     (256, 8192, 784), (300, 17000, 400), (512, 9000, 128), (500, 8200, 912), (700, 2050, 1152), (2000, 4096, 272),
     (260, 17500, 272), (512, 17408, 5120), (1025, 8196, 656), (1300, 6000, 400), (900, 4700, 144),
     (40, 33500, 144), (100, 33500, 272),
-    (1000, 17500, 272), (1024, 17408, 144)]          # the last two: columns left over from whole rounds
+    # columns left over from whole rounds, few to many
+    (1000, 17500, 272), (1024, 17408, 144), (1000, 19500, 272), (1024, 21900, 144), (16500, 1000, 144),
+    (1024, 26000, 144)]
 
 
 @pytest.mark.parametrize("M,N,K", WIDE)
