@@ -501,7 +501,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
 // counts each workgroup's slots per expert, the next adds the counts of the
 // workgroups before it (each for itself, up to 256 rows of E counts).
 constexpr int SORT_MAX_E = 1024, SORT_WAVES = 8, SORT_THREADS = 64 * SORT_WAVES;
-constexpr int SORT_ONE = 2048;       // slots up to which one workgroup does it all (4000: 8.3 us, with two launches 7.5)
+constexpr int SORT_ONE = 2048;       // slots up to which one workgroup does it all (2000: 5.9 us, two launches 6.3; 4000: 8.7, 6.6)
 constexpr int SORT_MAX_WGS = 256;
 
 // Per-wave counts of this workgroup's slots [s0, s1), run slots to a wave.
@@ -613,7 +613,9 @@ __global__ __launch_bounds__(SORT_THREADS) void moe_sort_one_kernel(
     sort_place(ids, 0, n, run, topk, E, bits, cnt, row_token, slot_row);
 }
 
-// hist [workgroups, E]
+// hist [workgroups, E], rows of whole 16-byte words, zeros behind E
+__device__ inline int hist_stride(int E) { return (E + 3) & ~3; }
+
 __global__ __launch_bounds__(SORT_THREADS) void moe_sort_count_kernel(
     const int32_t *__restrict__ ids, int n, int run, int E, int32_t *__restrict__ hist)
 {
@@ -621,11 +623,13 @@ __global__ __launch_bounds__(SORT_THREADS) void moe_sort_count_kernel(
     const int s0 = blockIdx.x * (run * SORT_WAVES);
     const int s1 = n - s0 < run * SORT_WAVES ? n : s0 + run * SORT_WAVES;
     sort_count(ids, s0, s1, run, E, cnt);
-    for (int e = threadIdx.x; e < E; e += SORT_THREADS) {
+    const int stride = hist_stride(E);
+    for (int e = threadIdx.x; e < stride; e += SORT_THREADS) {
         int a = 0;
+        if (e < E)
 #pragma unroll
-        for (int w = 0; w < SORT_WAVES; ++w) a += cnt[w][e];
-        hist[(size_t)blockIdx.x * E + e] = a;
+            for (int w = 0; w < SORT_WAVES; ++w) a += cnt[w][e];
+        hist[(size_t)blockIdx.x * stride + e] = a;
     }
 }
 
@@ -636,33 +640,42 @@ __global__ __launch_bounds__(SORT_THREADS) void moe_sort_place_kernel(
 {
     __shared__ int cnt[SORT_WAVES][SORT_MAX_E];
     __shared__ int tot[SORT_MAX_E], before[SORT_MAX_E], first[SORT_MAX_E + 1], sums[SORT_WAVES][2];
+    constexpr int BATCH = 16;
     const int tid = threadIdx.x, wgs = gridDim.x, me = blockIdx.x;
     const int s0 = me * (run * SORT_WAVES);
     const int s1 = n - s0 < run * SORT_WAVES ? n : s0 + run * SORT_WAVES;
-    for (int e = tid; e < E; e += SORT_THREADS) tot[e] = before[e] = 0;
+    const int stride = hist_stride(E), quads = stride / 4;
+    for (int e = tid; e < stride; e += SORT_THREADS) tot[e] = before[e] = 0;
     __syncthreads();
-    // The counts of all workgroups: the threads that E leaves over share the rows, and
-    // each thread's loads are in flight together (they come from other XCDs)
-    const int span = E > SORT_THREADS / 2 ? SORT_THREADS : E > 1 ? 1 << (32 - __builtin_clz(E - 1)) : 1;
-    const int parts = SORT_THREADS / span, part = tid / span;
-    for (int e = tid - part * span; e < E; e += span) {
-        int all = 0, mine = 0;
-        for (int w0 = part; w0 < wgs; w0 += 32 * parts) {
-            int c[32];
+    // The counts of all workgroups, four experts a thread; the threads that these leave
+    // over share the rows, and a thread's loads are in flight together (they come from
+    // other XCDs)
+    const int span = quads > 1 ? 1 << (32 - __builtin_clz(quads - 1)) : 1;      // at most 256
+    const int parts = SORT_THREADS / span, part = tid / span, quad = tid - part * span;
+    if (quad < quads) {
+        int4v all = {0, 0, 0, 0}, mine = all;
+        for (int w0 = part; w0 < wgs; w0 += BATCH * parts) {
+            int4v c[BATCH];
 #pragma unroll
-            for (int u = 0; u < 32; ++u) {
+            for (int u = 0; u < BATCH; ++u) {
                 const int w = w0 + u * parts;      // (past the end: the last row again, not counted)
-                c[u] = hist[(unsigned)(w < wgs ? w : wgs - 1) * E + e];
+                c[u] = reinterpret_cast<const int4v *>(hist)[(w < wgs ? w : wgs - 1) * quads + quad];
             }
 #pragma unroll
-            for (int u = 0; u < 32; ++u) {
+            for (int u = 0; u < BATCH; ++u) {
                 const int w = w0 + u * parts;
-                all += w < wgs ? c[u] : 0;
-                mine += w < me ? c[u] : 0;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    all[x] += w < wgs ? c[u][x] : 0;
+                    mine[x] += w < me ? c[u][x] : 0;
+                }
             }
         }
-        atomicAdd(&tot[e], all);
-        atomicAdd(&before[e], mine);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            atomicAdd(&tot[quad * 4 + x], all[x]);
+            atomicAdd(&before[quad * 4 + x], mine[x]);
+        }
     }
     sort_count(ids, s0, s1, run, E, cnt);      // (its barriers publish tot and before)
     sort_scan(sums, E, tot, first);
@@ -784,18 +797,21 @@ hipError_t launch_moe_route(const void *logits, int dtype, const float *bias, in
 }
 
 namespace {
-// Slots of one wave (a multiple of 64): 1024 slots to a workgroup until 256
-// workgroups would not do, one workgroup for few.  16383 x 8 slots of 256 experts:
-// 10.6 us (2048 a workgroup: 10.9, 512: 13.1), 2000 x 8 of 128: 8.2 (9.8, 7.3).
-int sort_run(long long n)
+// Slots of one wave (a multiple of 64): one workgroup for few slots; else 512 slots
+// to a workgroup, or 1024 where the counts of all that every workgroup reads
+// would be many; no more than 256 workgroups.  2000 x 8 slots of 128 experts: 7.3 us
+// (1024 a workgroup: 8.1, 2048: 9.6), 10000 x 8 of 67: 7.6 (8.3, 9.9), 16383 x 8 of
+// 256: 10.5 (9.2, 10.9), 12000 x 6 of 384: 11.1 (10.6, 10.9).
+int sort_run(long long n, int E)
 {
     if (n <= SORT_ONE) return (int)((n + SORT_THREADS - 1) / SORT_THREADS * 64);
+    const long long least = (n + SORT_THREADS - 1) / SORT_THREADS * E <= 24576 ? 64 : 128;
     const long long per = (n + (long long)SORT_MAX_WGS * SORT_THREADS - 1) / ((long long)SORT_MAX_WGS * SORT_THREADS) * 64;
-    return (int)(per < 128 ? 128 : per);
+    return (int)(per < least ? least : per);
 }
-int sort_wgs(long long n)
+int sort_wgs(long long n, int E)
 {
-    const long long per = (long long)sort_run(n) * SORT_WAVES;
+    const long long per = (long long)sort_run(n, E) * SORT_WAVES;
     return n <= SORT_ONE ? 1 : (int)((n + per - 1) / per);
 }
 } // namespace
@@ -803,7 +819,7 @@ int sort_wgs(long long n)
 size_t moe_sort_workspace_bytes(int T, int topk, int E)
 {
     const long long n = (long long)T * topk;
-    return n <= SORT_ONE ? 0 : W4A16_WS_COUNTER_BYTES + (size_t)sort_wgs(n) * E * sizeof(int32_t);
+    return n <= SORT_ONE ? 0 : W4A16_WS_COUNTER_BYTES + (size_t)sort_wgs(n, E) * ((E + 3) & ~3) * sizeof(int32_t);
 }
 
 hipError_t launch_moe_sort(const int32_t *ids, int T, int topk, int E, int32_t *offsets,
@@ -811,7 +827,7 @@ hipError_t launch_moe_sort(const int32_t *ids, int T, int topk, int E, int32_t *
 {
     int bits = 1;
     while ((1 << bits) <= E) ++bits;     // ids 0 .. E, E for a dropped slot
-    const int n = T * topk, run = sort_run(n), wgs = sort_wgs(n);
+    const int n = T * topk, run = sort_run(n, E), wgs = sort_wgs(n, E);
     if (wgs == 1) {
         hipLaunchKernelGGL(moe_sort_one_kernel, dim3(1), dim3(SORT_THREADS), 0, st, ids, n, run, topk, E, bits,
                            offsets, row_token, slot_row);
