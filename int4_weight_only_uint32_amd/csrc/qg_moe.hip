@@ -446,16 +446,14 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
     float my_c = 0.f;
     // with a bias one more than topk, to see that the last chosen is clear of it
     const int rounds = a.topk + (a.bias != nullptr ? 1 : 0);
-    if (!unsure)
+    uint2v *heads = reinterpret_cast<uint2v *>(sh[wave]);     // (at most VPL * 64 are found)
+    if (!unsure) {
         for (; found < rounds; ++found) {
             const unsigned m = wave_max(key[0]);
             if (m == 0) break;
             const int owner = __builtin_ctzll(__ballot(key[0] == m));
-            const int id = owner * VPL + (__builtin_amdgcn_readlane((int)order[0], owner) & 15);
-            const bool here = lane == found;
-            my_id = here ? id : my_id;
-            my_c = here ? key_value(m) : my_c;
             if (lane == owner) {
+                heads[found] = uint2v{m, (unsigned)e0 + (order[0] & 15)};
 #pragma unroll
                 for (int i = 0; i + 1 < VPL; ++i) key[i] = key[i + 1];
                 key[VPL - 1] = 0;
@@ -466,6 +464,15 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
                 }
             }
         }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        if (lane < found) {
+            const uint2v h = heads[lane];
+            my_c = key_value(h.x);
+            my_id = (int)h.y;
+        }
+    }
     if (a.bias) {
         const float after = __shfl_down(my_c, 1);
         const bool clear = my_c - after > route_error(sigmoid, my_c) + route_error(sigmoid, after);
