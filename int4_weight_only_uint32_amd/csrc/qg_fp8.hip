@@ -775,6 +775,15 @@ Fp8Kernel choose(bool grouped, int E, int M, int N, int K)
         if (w256 >= 192 || (w256 >= 128 && w > 256)) return T256x256;
         if (w > 128 && w <= 256) return T128x256;
     }
+    // 65 to 128 rows and many tiles: the large tile reads the weights once, and its waves
+    // without rows cost little.  100 rows at 5120 x 50257 (197 tiles): 81 us against 104
+    // (64 x 128); 100 an expert in 8 at 2048 x 7168 (224): 33 against 45, in 64: 262
+    // against 290.  Not where 64 x 128 is one round (three to a CU; 85 in 8 at 4096 x 6144:
+    // 63 against 56), large tiles leave over a quarter of their rounds empty (93 in 30 at
+    // 2048 x 3000: 63 against 59), K is short (70 in 60 at 1024 x 2048: 41 against 37) or,
+    // in several rounds, rows are few (75 in 32 at 2048 x 7168: 123 against 120).
+    const long long rounds = (w256 + 255) / 256;
+    if (K >= 2048 && w64 > 768 && w256 * 4 >= rounds * 256 * 3 && rows > (rounds == 1 ? 64 : 80)) return T256x256;
     // One tile to a CU at most: two groups over k.  256 rows at 4096 x 8192 (256 tiles):
     // 18.6 against 22.3; 64 rows (136): 34.4, 40.7, streaming 39.8; 300 rows at 2000 x
     // 3000 (235 tiles of 64 x 64): 10 against 14

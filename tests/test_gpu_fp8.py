@@ -243,7 +243,7 @@ WIDE = [
     (128, 8200, 656), (100, 17408, 1296), (128, 20000, 80), (200, 3000, 2000), (300, 3000, 112), (290, 5000, 656),
     (256, 8192, 784), (300, 17000, 400), (512, 9000, 128), (500, 8200, 912), (700, 2050, 1152), (2000, 4096, 272),
     (260, 17500, 272), (512, 17408, 5120), (1025, 8196, 656), (1300, 6000, 400), (900, 4700, 144),
-    (40, 33500, 144), (100, 33500, 272),
+    (40, 33500, 144), (100, 33500, 272), (100, 50257, 2064),
     # columns left over from whole rounds, few to many
     (1000, 17500, 272), (1024, 17408, 144), (1000, 19500, 272), (1024, 21900, 144), (16500, 1000, 144),
     (1024, 26000, 144)]
@@ -302,6 +302,10 @@ GROUPED = [
     ([129, 0, 700, 200, 90, 333], 8200, 272, 700, 3, 2),
     ([1, 2, 3, 0, 16, 17, 5, 9], 16400, 272, 40, 0, 1),
     ([30, 20, 31, 0, 70, 17, 5, 9], 16400, 144, 40, 0, 1),
+    # few rows an expert on the large tile; experts of more row blocks than one band, large tile and small
+    ([64, 1, 0, 65, 128, 257, 100, 140], 7300, 2064, 300, 1, 2),
+    ([1700, 5, 300], 8200, 144, 900, 0, 3),
+    ([0] * 12 + [1700] + [0] * 17, 600, 144, 400, 0, 0),
 ]
 
 
