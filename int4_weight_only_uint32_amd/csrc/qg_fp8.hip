@@ -723,7 +723,7 @@ long long row_blocks(bool grouped, int E, int M, int BM)
 // the tiled ones by their tile.
 enum Fp8Kernel {
     S1x2x4, S1x2x2, S1x1x4, S2x2x4, S2x4x2, S4x2x4, S4x4x4,
-    T64x64K2, T64x128, T64x128K2, T128x128K2, T128x256, T256x256
+    T64x64K2, T64x128, T64x128K2, T128x128K2, T128x256W4, T128x256, T256x256
 };
 
 struct Fp8Shape {
@@ -737,7 +737,8 @@ constexpr Fp8Shape FP8_SHAPES[] = {
     {"streaming, 64 x 64, 4 waves over k", 64, 64, 256},
     {"tiled, 64 x 64, 2 groups over k", 64, 64, 512},     {"tiled, 64 x 128", 64, 128, 256},
     {"tiled, 64 x 128, 2 groups over k", 64, 128, 512},   {"tiled, 128 x 128, 2 groups over k", 128, 128, 512},
-    {"tiled, 128 x 256", 128, 256, 256},                  {"tiled, 256 x 256", 256, 256, 512}};
+    {"tiled, 128 x 256, 4 waves", 128, 256, 256},         {"tiled, 128 x 256", 128, 256, 512},
+    {"tiled, 256 x 256", 256, 256, 512}};
 
 // By the rows an expert has on average (the host does not know the counts; an
 // uneven split is slower, never wrong) and the workgroups that makes.  Both
@@ -773,7 +774,9 @@ Fp8Kernel choose(bool grouped, int E, int M, int N, int K)
         // (256 or 128): 40 against 51
         const long long w = wgs(128, 256);
         if (w256 >= 192 || (w256 >= 128 && w > 256)) return T256x256;
-        if (w > 128 && w <= 256) return T128x256;
+        // four waves read less from LDS, eight wait less: 1024 rows at 8192 columns, K = 2048
+        // 23.9 and 22.9, 5120 56 and 58; 256 at 17408 columns, K = 2048 22.7 and 20.9
+        if (w > 128 && w <= 256) return K <= 4096 ? T128x256 : T128x256W4;
     }
     // 65 to 128 rows and many tiles: the large tile reads the weights once, and its waves
     // without rows cost little.  100 rows at 5120 x 50257 (197 tiles): 81 us against 104
@@ -886,7 +889,8 @@ hipError_t launch(const Fp8Args &a, hipStream_t st)
     case T64x128: return tiled<64, 128, 2, 2, 1, BF16>(a, st);
     case T64x128K2: return tiled<64, 128, 2, 2, 2, BF16>(a, st);
     case T128x128K2: return tiled<128, 128, 2, 2, 2, BF16>(a, st);
-    case T128x256: return tiled<128, 256, 2, 2, 1, BF16>(a, st);
+    case T128x256W4: return tiled<128, 256, 2, 2, 1, BF16>(a, st);
+    case T128x256: return tiled<128, 256, 2, 4, 1, BF16>(a, st);
     case T256x256: return large_tiles<BF16>(a, st);
     }
     return hipErrorUnknown;

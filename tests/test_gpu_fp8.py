@@ -241,7 +241,7 @@ WIDE = [
     (3, 65540, 272), (16, 65600, 4112), (9, 4100, 4112), (16, 4096, 1040), (20, 65600, 272), (32, 70000, 144),
     (40, 4100, 272), (64, 5120, 4240), (100, 4100, 4240), (128, 2050, 1168), (50, 16500, 400), (64, 20000, 128),
     (128, 8200, 656), (100, 17408, 1296), (128, 20000, 80), (200, 3000, 2000), (300, 3000, 112), (290, 5000, 656),
-    (256, 8192, 784), (300, 17000, 400), (512, 9000, 128), (500, 8200, 912), (700, 2050, 1152), (2000, 4096, 272),
+    (256, 8192, 784), (300, 17000, 400), (300, 17000, 4112), (512, 9000, 128), (500, 8200, 912), (700, 2050, 1152), (2000, 4096, 272),
     (260, 17500, 272), (512, 17408, 5120), (1025, 8196, 656), (1300, 6000, 400), (900, 4700, 144),
     (40, 33500, 144), (100, 33500, 272), (100, 50257, 2064),
     # columns left over from whole rounds, few to many
