@@ -509,16 +509,21 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
 // counts each workgroup's slots per expert, the next adds the counts of the
 // workgroups before it (each for itself, up to 256 rows of E counts).
 constexpr int SORT_MAX_E = 1024, SORT_WAVES = 8, SORT_THREADS = 64 * SORT_WAVES;
-constexpr int SORT_ONE = 2048;       // slots up to which one workgroup does it all (2000: 5.9 us, two launches 6.3; 4000: 8.7, 6.6)
+// Slots up to which one workgroup does it all, of 8 waves, or for up to 512 experts (whose
+// counts of 16 waves LDS holds) of 16 from 1025 slots on.  In a graph: 1024 slots of 256
+// experts 4.3 us (8 waves) and 4.5 (16), 2000 of 64 5.9 and 5.3, with two launches 6.3;
+// 4000 7.0 (16 waves) and 6.5 (two launches), which outside a graph are the host's 10.6.
+constexpr int SORT_ONE = 2048, SORT_ONE_WIDE = 4096, SORT_WIDE_E = 512, SORT_WIDE_FROM = 1024;
 constexpr int SORT_MAX_WGS = 256;
 
 // Per-wave counts of this workgroup's slots [s0, s1), run slots to a wave.
+template <int WAVES, int MAX_E>
 __device__ inline void sort_count(const int32_t *__restrict__ ids, int s0, int s1, int run, int E,
-                                  int (*cnt)[SORT_MAX_E])
+                                  int (&cnt)[WAVES][MAX_E])
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int w = 0; w < SORT_WAVES; ++w)
-        for (int e = tid; e < E; e += SORT_THREADS) cnt[w][e] = 0;
+    for (int w = 0; w < WAVES; ++w)
+        for (int e = tid; e < E; e += 64 * WAVES) cnt[w][e] = 0;
     __syncthreads();
     const int a = s0 + wave * run, b = a + run < s1 ? a + run : s1;
 #pragma unroll 4
@@ -531,7 +536,8 @@ __device__ inline void sort_count(const int32_t *__restrict__ ids, int s0, int s
 
 // Exclusive prefix over the experts of the totals, two of them a thread; out[E]
 // is the sum.  Every thread of the workgroup calls it.
-__device__ inline void sort_scan(int (*sums)[2], int E, const int *tot, int *out)
+template <int WAVES>
+__device__ inline void sort_scan(int (&sums)[WAVES], int E, const int *tot, int *out)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int e = 2 * tid;
@@ -542,22 +548,23 @@ __device__ inline void sort_scan(int (*sums)[2], int E, const int *tot, int *out
         const int v = __shfl_up(x, o);
         if (lane >= o) x += v;
     }
-    if (lane == 63) sums[wave][0] = x;
+    if (lane == 63) sums[wave] = x;
     __syncthreads();
     int before = 0;
 #pragma unroll
-    for (int w = 0; w < SORT_WAVES; ++w)
-        if (w < wave) before += sums[w][0];
+    for (int w = 0; w < WAVES; ++w)
+        if (w < wave) before += sums[w];
     const int at = before + x - t0 - t1;
     if (e <= E) out[e] = at;
     if (e + 1 <= E) out[e + 1] = at + t0;
-    if (tid == SORT_THREADS - 1 && E == 2 * SORT_THREADS) out[E] = at + t0 + t1;
+    if (tid == 64 * WAVES - 1 && E == 128 * WAVES) out[E] = at + t0 + t1;
     __syncthreads();
 }
 
 // Places the workgroup's slots: cnt[w][e] is the row of wave w's next slot of e.
+template <int WAVES, int MAX_E>
 __device__ inline void sort_place(const int32_t *__restrict__ ids, int s0, int s1, int run, int topk,
-                                  int E, int bits, int (*cnt)[SORT_MAX_E],
+                                  int E, int bits, int (&cnt)[WAVES][MAX_E],
                                   int32_t *__restrict__ row_token, int32_t *__restrict__ slot_row)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -590,28 +597,29 @@ __device__ inline void sort_place(const int32_t *__restrict__ ids, int s0, int s
     }
 }
 
-__global__ __launch_bounds__(SORT_THREADS) void moe_sort_one_kernel(
+template <int WAVES, int MAX_E>
+__global__ __launch_bounds__(64 * WAVES) void moe_sort_one_kernel(
     const int32_t *__restrict__ ids, int n, int run, int topk, int E, int bits,
     int32_t *__restrict__ offsets, int32_t *__restrict__ row_token, int32_t *__restrict__ slot_row)
 {
-    __shared__ int cnt[SORT_WAVES][SORT_MAX_E];
-    __shared__ int tot[SORT_MAX_E], first[SORT_MAX_E + 1], sums[SORT_WAVES][2];
+    __shared__ int cnt[WAVES][MAX_E];
+    __shared__ int tot[MAX_E], first[MAX_E + 1], sums[WAVES];
     const int tid = threadIdx.x;
     sort_count(ids, 0, n, run, E, cnt);
-    for (int e = tid; e < E; e += SORT_THREADS) {
+    for (int e = tid; e < E; e += 64 * WAVES) {
         int a = 0;
 #pragma unroll
-        for (int w = 0; w < SORT_WAVES; ++w) a += cnt[w][e];
+        for (int w = 0; w < WAVES; ++w) a += cnt[w][e];
         tot[e] = a;
     }
     __syncthreads();
     sort_scan(sums, E, tot, first);
-    for (int e = tid; e <= E; e += SORT_THREADS) {
+    for (int e = tid; e <= E; e += 64 * WAVES) {
         int at = first[e];
         offsets[e] = at;
         if (e < E)
 #pragma unroll
-            for (int w = 0; w < SORT_WAVES; ++w) {
+            for (int w = 0; w < WAVES; ++w) {
                 const int c = cnt[w][e];
                 cnt[w][e] = at;
                 at += c;
@@ -647,7 +655,7 @@ __global__ __launch_bounds__(SORT_THREADS) void moe_sort_place_kernel(
     int32_t *__restrict__ slot_row)
 {
     __shared__ int cnt[SORT_WAVES][SORT_MAX_E];
-    __shared__ int tot[SORT_MAX_E], before[SORT_MAX_E], first[SORT_MAX_E + 1], sums[SORT_WAVES][2];
+    __shared__ int tot[SORT_MAX_E], before[SORT_MAX_E], first[SORT_MAX_E + 1], sums[SORT_WAVES];
     constexpr int BATCH = 16;
     const int tid = threadIdx.x, wgs = gridDim.x, me = blockIdx.x;
     const int s0 = me * (run * SORT_WAVES);
@@ -806,29 +814,30 @@ hipError_t launch_moe_route(const void *logits, int dtype, const float *bias, in
 }
 
 namespace {
-// Slots of one wave (a multiple of 64): one workgroup for few slots; else 512 slots
+// Slots of one wave (a multiple of 64) of several workgroups: 512 slots
 // to a workgroup, or 1024 where the counts of all that every workgroup reads
 // would be many; no more than 256 workgroups.  2000 x 8 slots of 128 experts: 7.3 us
 // (1024 a workgroup: 8.1, 2048: 9.6), 10000 x 8 of 67: 7.6 (8.3, 9.9), 16383 x 8 of
 // 256: 10.5 (9.2, 10.9), 12000 x 6 of 384: 11.1 (10.6, 10.9).
 int sort_run(long long n, int E)
 {
-    if (n <= SORT_ONE) return (int)((n + SORT_THREADS - 1) / SORT_THREADS * 64);
     const long long least = (n + SORT_THREADS - 1) / SORT_THREADS * E <= 24576 ? 64 : 128;
     const long long per = (n + (long long)SORT_MAX_WGS * SORT_THREADS - 1) / ((long long)SORT_MAX_WGS * SORT_THREADS) * 64;
     return (int)(per < least ? least : per);
 }
 int sort_wgs(long long n, int E)
 {
+    if (n <= (E <= SORT_WIDE_E ? SORT_ONE_WIDE : SORT_ONE)) return 1;
     const long long per = (long long)sort_run(n, E) * SORT_WAVES;
-    return n <= SORT_ONE ? 1 : (int)((n + per - 1) / per);
+    return (int)((n + per - 1) / per);
 }
 } // namespace
 
 size_t moe_sort_workspace_bytes(int T, int topk, int E)
 {
     const long long n = (long long)T * topk;
-    return n <= SORT_ONE ? 0 : W4A16_WS_COUNTER_BYTES + (size_t)sort_wgs(n, E) * ((E + 3) & ~3) * sizeof(int32_t);
+    const int wgs = sort_wgs(n, E);
+    return wgs == 1 ? 0 : W4A16_WS_COUNTER_BYTES + (size_t)wgs * ((E + 3) & ~3) * sizeof(int32_t);
 }
 
 hipError_t launch_moe_sort(const int32_t *ids, int T, int topk, int E, int32_t *offsets,
@@ -836,12 +845,17 @@ hipError_t launch_moe_sort(const int32_t *ids, int T, int topk, int E, int32_t *
 {
     int bits = 1;
     while ((1 << bits) <= E) ++bits;     // ids 0 .. E, E for a dropped slot
-    const int n = T * topk, run = sort_run(n, E), wgs = sort_wgs(n, E);
+    const int n = T * topk, wgs = sort_wgs(n, E);
     if (wgs == 1) {
-        hipLaunchKernelGGL(moe_sort_one_kernel, dim3(1), dim3(SORT_THREADS), 0, st, ids, n, run, topk, E, bits,
-                           offsets, row_token, slot_row);
+#define QG_SORT_ONE(WAVES, MAX_E) \
+    hipLaunchKernelGGL((moe_sort_one_kernel<WAVES, MAX_E>), dim3(1), dim3(64 * WAVES), 0, st, ids, n, \
+                       (n + 64 * WAVES - 1) / (64 * WAVES) * 64, topk, E, bits, offsets, row_token, slot_row)
+        if (E <= SORT_WIDE_E && n > SORT_WIDE_FROM) QG_SORT_ONE(16, SORT_WIDE_E);
+        else QG_SORT_ONE(SORT_WAVES, SORT_MAX_E);
+#undef QG_SORT_ONE
         return hipGetLastError();
     }
+    const int run = sort_run(n, E);
     int32_t *hist = (int32_t *)((char *)ws + W4A16_WS_COUNTER_BYTES);
     hipLaunchKernelGGL(moe_sort_count_kernel, dim3(wgs), dim3(SORT_THREADS), 0, st, ids, n, run, E, hist);
     const hipError_t e = hipGetLastError();

@@ -210,7 +210,7 @@ def check_sort(ids, E):
 
 @pytest.mark.parametrize("T,k,E", [
     (1, 1, 1), (1, 8, 64), (16, 8, 64), (5, 3, 4), (64, 1, 8), (65, 1, 1024), (100, 7, 60), (129, 8, 256), (257, 8, 256),
-    (511, 8, 384), (513, 8, 384), (1000, 6, 160), (2049, 8, 257), (4099, 8, 1024), (16383, 8, 256), (70001, 2, 8),
+    (511, 8, 384), (513, 8, 384), (512, 8, 512), (500, 8, 513), (1500, 1, 500), (4096, 1, 3), (1000, 6, 160), (2049, 8, 257), (4099, 8, 1024), (16383, 8, 256), (70001, 2, 8),
     (40000, 9, 128)])
 def test_sort(T, k, E):
     note(f"sort T={T} k={k} E={E}")
