@@ -395,7 +395,8 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
                 above += x > hi;
                 not_below += x >= lo;
             }
-            unsure = __ballot(group && above < a.topk_group && not_below >= a.topk_group) != 0;
+            // (sums past binary32's range, or an infinite bias: no order without 64 bits)
+            unsure = !(tol < __builtin_inff()) || __ballot(group && above < a.topk_group && not_below >= a.topk_group) != 0;
             stays = not_below < a.topk_group;
         } else {
             int before = 0;
