@@ -324,10 +324,11 @@ int quantize_rows_int8(const uint16_t *A, int M, int K, int8_t *A_q, float *a_sc
  *            a_scale[m,b] = max |x| / 448
  *            A_q[m,k]     = e4m3(clamp(x[m,k] / a_scale[m,b], -448, 448))
  *          both quotients rounded once to binary32, the code rounded to the
- *          nearest (ties to even).  A block of zeros gets scale 0 and
- *          codes 0; a block with a NaN, an infinity or an x beyond
- *          binary32's range gets a NaN scale and NaN codes, so every product
- *          with it is NaN.
+ *          nearest (ties to even).  A block of zeros, of either sign, or
+ *          of values so small that max |x| / 448 rounds to 0 gets scale 0
+ *          and codes 0 (the byte 0x00); a block with a NaN, an infinity or
+ *          an x beyond binary32's range gets a NaN scale and NaN codes, so
+ *          every product with it is NaN.
  * M == 0 is a call that does nothing.  One kernel on `stream`, no workspace. */
 #define QG_QUANT_SWIGLU 0x1u
 int quantize_rows_fp8(const void *A, int dtype, int M, int K, unsigned flags, uint8_t *A_q,

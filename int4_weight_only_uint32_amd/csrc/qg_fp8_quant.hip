@@ -188,6 +188,8 @@ __global__ __launch_bounds__(256) void quantize_rows_fp8_kernel(
             }
         }
     }
+    // no scale, no sign either: -0 and what is too small for a scale are the byte 0 too
+    if (sc == 0.0f) o = uint2v{0u, 0u};
     __builtin_nontemporal_store(o, reinterpret_cast<uint2v *>(Aq + at));
 }
 #undef QG_ROW_MAX
