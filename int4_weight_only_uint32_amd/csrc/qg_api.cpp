@@ -590,7 +590,7 @@ int quantize_rows_fp8(const void *A, int dtype, int M, int K, unsigned flags, ui
     if (M < 0 || K < 1)
         return fail(QG_ERR_INVALID_ARG, "%s: M >= 0 and K >= 1 needed (got %d, %d)", what, M, K);
     if (K % 16) return fail(QG_ERR_UNSUPPORTED, "%s: K must be a multiple of 16 (got %d)", what, K);
-    if ((long long)M * ((K + 127) / 128) * 16 > MAX_GRID_THREADS - 256)
+    if (M * ((K + 127ll) / 128) * 16 > MAX_GRID_THREADS - 256)
         return fail(QG_ERR_UNSUPPORTED, "%s: M=%d, K=%d too large", what, M, K);
     if (flags & ~QG_QUANT_SWIGLU) return fail(QG_ERR_INVALID_ARG, "%s: unknown flags 0x%x", what, flags);
     if (M == 0) return ok();

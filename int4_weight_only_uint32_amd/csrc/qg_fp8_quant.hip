@@ -202,7 +202,7 @@ hipError_t launch_quantize_rows_fp8(const void *A, int dtype, int M, int K, bool
 {
     QuantShape q;
     q.K = K;
-    q.KB = (K + 127) / 128;
+    q.KB = (int)((K + 127ll) / 128);      // (K up to 2^31 - 16)
     q.blocks = (unsigned)M * (unsigned)q.KB;
     // blk < 2^28: magic = ceil(2^(29 + l) / KB) <= 2^30 with 2^l >= KB is off by less
     // than blk * KB / 2^(29 + l) < 1 part of a block
