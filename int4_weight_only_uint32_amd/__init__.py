@@ -434,6 +434,16 @@ def _arg(t: Optional[torch.Tensor], dtype, shape, dev, name):
     raise ValueError(f"{name} is on {t.device}, not on GPU {dev}")
 
 
+def _scratch(t: Optional[torch.Tensor], dev):
+    """Pointer and bytes of a workspace on GPU `dev`."""
+    p = _ptr(t, None, "workspace")
+    if p is None:
+        return None, 0
+    if t.get_device() != dev:
+        raise ValueError(f"workspace is on {t.device}, not on GPU {dev}")
+    return p, t.numel() * t.element_size()
+
+
 # The handle of a device's current stream and the current device's index without
 # the objects that torch.cuda makes of them (2 us of a 7 us call), where torch
 # has these.
@@ -511,8 +521,7 @@ def qgemm_fp8(A_q, a_scale, a_rows, M_a, W, w_scale, expert_offsets, num_experts
           _arg(W, torch.float8_e4m3fn, (N, K) if one else (E, N, K), dev, "W"),
           _arg(w_scale, torch.float32, (NB, KB) if one else (E, NB, KB), dev, "w_scale"),
           _arg(expert_offsets, torch.int32, (E + 1,), dev, "expert_offsets"), E, M_total, N, K, d,
-          _arg(C, None, (M_total, N), dev, "C"), _ptr(workspace, None, "workspace"),
-          0 if workspace is None else workspace.numel() * workspace.element_size(), flags)
+          _arg(C, None, (M_total, N), dev, "C"), *_scratch(workspace, dev), flags)
 
 
 def fp8_gemm(A_q: torch.Tensor, a_scale: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor,
@@ -572,8 +581,7 @@ def moe_sort_rows(ids, T, topk, num_experts, expert_offsets, row_token, slot_row
     _call(lib().moe_sort_rows, dev, _arg(ids, torch.int32, (T, topk), dev, "ids"), T, topk, num_experts,
           _arg(expert_offsets, torch.int32, (num_experts + 1,), dev, "expert_offsets"),
           _arg(row_token, torch.int32, (T * topk,), dev, "row_token"),
-          _arg(slot_row, torch.int32, (T, topk), dev, "slot_row"), _ptr(workspace, None, "workspace"),
-          0 if workspace is None else workspace.numel() * workspace.element_size())
+          _arg(slot_row, torch.int32, (T, topk), dev, "slot_row"), *_scratch(workspace, dev))
 
 
 @functools.lru_cache(maxsize=1024)
