@@ -242,6 +242,8 @@ __device__ __forceinline__ void fp8_tile(
             const int more = k + (q - LA) * 8 * K;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(w_rs, (__attribute__((address_space(3))) void *)dst, 16, off, more, 0, 0);
         }
+        // (the waiting build: each load lands before the next MFMA, none at the barrier)
+        debug_stage_sync();
     };
 
     // Scales, four steps at a time: lane l loads, for its row (l % 16) of each
@@ -378,7 +380,6 @@ __device__ __forceinline__ void fp8_tile(
             if (j == NT - 1) {
                 // every load of step kt + 1 has landed and every read of step kt is done
                 __builtin_amdgcn_s_waitcnt(0);
-                debug_stage_sync();
                 __syncthreads();
                 if (at == 3) keep_scales();
 #pragma unroll
@@ -481,6 +482,7 @@ __device__ __forceinline__ void fp8_tile(
             }
         // (the wave reads back its own words, in order)
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        debug_stage_sync();
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll

@@ -151,6 +151,7 @@ __device__ inline void route_exact(const RouteArgs &a, int t, double *sh)
             sh[lane * VPL + i] = !a.bias && sums && choice[i] != NINF ? score[i] : choice[i];
         // the wave's own words only, in order: no other wave to wait for
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        debug_stage_sync();
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         double v = NINF, v2 = NINF;
@@ -362,6 +363,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
             for (int i = 0; i < VPL; ++i) vals[e0 + i] = v[i];
             // (the wave's own words, in order: no other wave to wait for)
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            debug_stage_sync();
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
             if (lane < a.n_group)
@@ -370,6 +372,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
                     v2 = __builtin_fmaxf(v2, __builtin_fminf(v1, x));
                     v1 = __builtin_fmaxf(v1, x);
                 }
+            debug_stage_sync();
             __builtin_amdgcn_wave_barrier();
         }
         const bool group = mine < a.n_group;
@@ -467,6 +470,7 @@ __global__ __launch_bounds__(256) void moe_route_kernel(RouteArgs a, int wide, i
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        debug_stage_sync();
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         if (lane < found) {
@@ -588,8 +592,10 @@ __device__ inline void sort_place(const int32_t *__restrict__ ids, int s0, int s
         // before the lowest lane of each expert raises it
         int row = -1;
         if (id < E) row = next[id] + __popcll(same & below);
+        debug_stage_sync();
         __builtin_amdgcn_wave_barrier();
         if (id < E && (same & below) == 0) next[id] = row + __popcll(same);
+        debug_stage_sync();
         __builtin_amdgcn_wave_barrier();
         if (s < b) {
             slot_row[s] = row;
