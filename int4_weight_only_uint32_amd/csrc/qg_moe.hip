@@ -231,12 +231,16 @@ __device__ inline void route_exact(const RouteArgs &a, int t, double *sh)
     route_store(a, t, lane, my_id, (float)(w * (double)a.scaling));
 }
 
-// How far a choice c in 32 bits may be from its value: the scores' error (below
-// 1; the exponential's 2^-22, a reciprocal and a few roundings for the
-// sigmoid: 2^-20 holds them; for softmax the sum's terms add their own
-// exponents' roundings, |l - max| 2^-24 each, under 8 of them on a
-// probability's average, and 22 roundings of the sum: 2^-18) and the
-// rounding of the sum with the bias.
+// How far a choice c in 32 bits may be from its value, at most: the score's error
+// and the rounding of its sum with the bias (half a step, 2^-24 |c|; the rest of
+// 1.0625 is for the roundings of the bound itself).  The scores' errors, in units of 2^-24:
+//   sigmoid, s = 1 / d, d = 1 + e: e is off by 4 e (exp_near), which is 4 s (1 - s) of s;
+//   d by half a step, 1 for d < 2, which is s^2; the reciprocal by a step, 1 under
+//   s = 1: together at most 2.34, at s = 2/3, and less under 1/2.  Taken as 4, 2^-22.
+//   softmax, p = e / sum: e is off by 4 e and |l - max| e (its argument's rounding);
+//   the sum by 4, by 22 roundings (16 experts a lane, six joins) and by the mean of
+//   |l - max|, which is at most ln 1024 < 7 (entropy); p by 2 (reciprocal) and 1; and p |l - max|
+//   is under 0.4: 41 in all.  Taken as 64, 2^-18.
 __device__ inline float route_error(bool sigmoid, float c)
 {
     return (sigmoid ? 0x1p-22f : 0x1p-18f) + 0x1.1p-24f * __builtin_fabsf(c);
