@@ -18,8 +18,13 @@ namespace {
 constexpr int KB8 = 128;   // k extent of a scale block, bytes of a tile row
 
 // An offset past every buffer range here (a block's rows, or with a row index all
-// of A: at most 2^32 - 2^23 bytes, which the caller checks), also after a step's scalar offset (below 2^22 + 256) is added.
+// of A: at most 2^32 - 2^23 bytes, which the caller checks) that does not wrap when
+// a step's scalar offset is added.  Those go past the last of the at most 2^15 k blocks by
+// the steps asked for ahead: MAX_AHEAD bounds them, and each kernel checks its own.
 constexpr unsigned FP8_PAST = 0xFFBFFFF0u - 0x1000u;
+constexpr int MAX_AHEAD = 16;
+static_assert(FP8_PAST > 0xFFFFFFFFu - (1u << 23) && (1u << 15) * KB8 + MAX_AHEAD * KB8 + 16 <= 0xFFFFFFFFu - FP8_PAST,
+              "past every range, and no wrap");
 // The same for a tile of W: at most 256 rows, 2^30 bytes, and scalar offsets
 // up to such a tile.
 constexpr unsigned FP8_W_PAST = 0x80000000u;
@@ -176,6 +181,8 @@ __device__ __forceinline__ void fp8_tile(
     constexpr int NW = WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
     constexpr int LA = BM / 8 / NW, LW = BN / 8 / NW;    // 1 KB loads per wave and step
     static_assert(LA * NW * 8 == BM && LW * NW * 8 == BN, "whole loads per wave");
+    // (KS groups' steps end within KS - 1 blocks past the last, two more steps are asked for)
+    static_assert(3 * KS - 1 <= MAX_AHEAD, "the scalar offset of the last load");
     static_assert(BN / WN <= 128 && 128 % (BN / WN) == 0, "a wave's columns share one weight scale");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds_all[];
     constexpr int STAGE = (BM + BN) * KB8;
@@ -567,6 +574,7 @@ __global__ __launch_bounds__(64 * NW) void fp8_stream_kernel(
     constexpr int STAGE = (BN + BM) * KB8 + 512;                 // tiles, then 64 row scales, then the weight's
     static_assert(MT <= 4 && 128 % BN == 0, "one load for the rows' scales, one weight scale");
     static_assert((P - 1) * L < 64, "vmcnt holds 6 bits");
+    static_assert((2 * P - 1) * NW <= MAX_AHEAD, "the scalar offset of the last refill");
     static_assert(MT * NT * 1024 <= P * STAGE, "the partial sums fit in the ring");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int nbn = (N + BN - 1) / BN;
