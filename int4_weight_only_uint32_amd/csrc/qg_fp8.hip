@@ -8,6 +8,7 @@
 // a lane's four results are four consecutive n of one row m: they share one
 // activation scale, and store as one 8-byte word.
 #include <cstdio>
+#include <cstring>
 
 #include "qg_device.h"
 #include "qg_launch.h"
@@ -861,19 +862,32 @@ hipError_t two_tiles(const Fp8Args &a, int nbn, hipStream_t st)
 //     48        112         101          90         104
 //     88        120         129         120         113
 //    152        126                                 147
+struct LargeSplit {
+    int nbn;             // column blocks of large tiles, 0 for all of them
+    Fp8Kernel rest;      // the tile of the other columns
+};
+
+LargeSplit large_split(bool grouped, int M, int N)
+{
+    const long long rbs = (M + 255) / 256, tiles = rbs * ((N + 255) / 256);
+    const int nbn = (int)(tiles / 256 * 256 / rbs);
+    const long long cols = N - (long long)nbn * 256;
+    if (grouped || nbn == 0 || cols <= 0) return {0, T256x256};
+    for (const Fp8Kernel rest : {T64x128K2, T128x128K2, T128x256}) {
+        const Fp8Shape &k = FP8_SHAPES[rest];
+        if (((M + k.bm - 1) / k.bm) * ((cols + k.bn - 1) / k.bn) <= 256) return {nbn, rest};
+    }
+    return {0, T256x256};
+}
+
 template <bool BF16>
 hipError_t large_tiles(const Fp8Args &a, hipStream_t st)
 {
-    const long long rbs = (a.M + 255) / 256, tiles = rbs * ((a.N + 255) / 256);
-    const int nbn = (int)(tiles / 256 * 256 / rbs);
-    const long long cols = a.N - (long long)nbn * 256;
-    auto small = [&](int bm, int bn) { return ((a.M + bm - 1) / bm) * ((cols + bn - 1) / bn); };
-    if (!a.offsets && nbn > 0 && cols > 0) {
-        if (small(64, 128) <= 256) return two_tiles<64, 128, 2, 2, 2, BF16>(a, nbn, st);
-        if (small(128, 128) <= 256) return two_tiles<128, 128, 2, 2, 2, BF16>(a, nbn, st);
-        if (small(128, 256) <= 256) return two_tiles<128, 256, 2, 4, 1, BF16>(a, nbn, st);
-    }
-    return tiled<256, 256, 4, 2, 1, BF16>(a, st);
+    const LargeSplit x = large_split(a.offsets != nullptr, a.M, a.N);
+    if (x.nbn == 0) return tiled<256, 256, 4, 2, 1, BF16>(a, st);
+    if (x.rest == T64x128K2) return two_tiles<64, 128, 2, 2, 2, BF16>(a, x.nbn, st);
+    if (x.rest == T128x128K2) return two_tiles<128, 128, 2, 2, 2, BF16>(a, x.nbn, st);
+    return two_tiles<128, 256, 2, 4, 1, BF16>(a, x.nbn, st);
 }
 
 template <int MT, int NT, int NW, int P, bool BF16>
@@ -930,7 +944,13 @@ long long fp8_threads(bool grouped, int E, int M, int N, int K)
 
 void describe_fp8(bool grouped, int E, int M, int N, int K, char *buf, size_t n)
 {
-    snprintf(buf, n, "%s", FP8_SHAPES[choose(grouped, E, M, N, K)].name);
+    const Fp8Kernel kern = choose(grouped, E, M, N, K);
+    const LargeSplit x = kern == T256x256 ? large_split(grouped, M, N) : LargeSplit{0, kern};
+    if (x.nbn)
+        snprintf(buf, n, "%s, from column %d on %s", FP8_SHAPES[kern].name, x.nbn * 256,
+                 FP8_SHAPES[x.rest].name + strlen("tiled, "));
+    else
+        snprintf(buf, n, "%s", FP8_SHAPES[kern].name);
 }
 
 } // namespace qg
