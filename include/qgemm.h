@@ -384,7 +384,12 @@ int qgemm_fp8(const uint8_t *A_q, const float *a_scale, const int32_t *a_rows, i
  *          groups (the order of the scores, also where those saturate).
  *          Equal ones go to the lowest index.
  * weights  [T,topk] fp32 out: s[t,ids], with QG_ROUTE_RENORMALIZE divided by
- *          their sum over the token's chosen experts, times `scaling`.
+ *          their sum over the token's chosen experts (0 where that sum is 0),
+ *          times `scaling`.  Computed in binary32, each within (41 + d) 2^-24
+ *          of its size, d the distance of its logit from the token's largest
+ *          (softmax), or 24 * 2^-24 (sigmoid).  A token with a
+ *          score under 2^-120 among its chosen, or one whose order 32 bits
+ *          leave open, has its weights from 64 bits, rounded once.
  * An expert whose logit is -infinity or NaN, or whose choice is, is masked: it
  * is never chosen, and slots left over hold id -1 and weight 0 (moe_sort_rows
  * drops them).  A logit of +infinity counts as the largest, in equal shares.
