@@ -168,7 +168,7 @@ __device__ inline void store4(uint16_t *c, float4v x, bool zero, int n, int N, b
 // KS > 1: KS such groups of waves, each with LDS of its own, take the steps in
 // turn, and their sums meet in LDS in the order of the groups; for grids that
 // leave CUs idle or K long, where a step's latency is what counts.
-// 4096 x 5120 x 17408: 332 to 339 us, 2.2 PFLOP/s of the 3.45 that MFMAs with four FMAs
+// 4096 x 5120 x 17408 (M x K x N): 332 to 348 us, 2.1 to 2.2 PFLOP/s of the 3.45 that MFMAs with four FMAs
 // each reach from registers alone; a third of the waves' time is spent at the step's
 // barrier, for loads that come from beyond L2 (with L2 hits only 10 % faster).
 // b: the workgroup's number among those of this tile.
@@ -528,7 +528,8 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void fp8_tiled_kernel(
 
 // Dense, the first `large` workgroups 256 x 256 tiles of the first nbn column blocks,
 // the others BM x BN tiles of the rest, in one launch: a CU that has done its
-// large tiles begins with a small one (4096 x 17408 x 5120: 349 us, as two launches 353).
+// large tiles begins with a small one (M x K x N = 4096 x 17408 x 5120: 349 us, as two
+// launches 353).
 template <int BM, int BN, int WM, int WN, int KS, bool BF16>
 __global__ __launch_bounds__(512) void fp8_two_tiles_kernel(
     const uint8_t *__restrict__ Aall, const float *__restrict__ a_scale,
@@ -785,9 +786,9 @@ Fp8Kernel choose(bool grouped, int E, int M, int N, int K)
         return S4x4x4;
     }
     if (rows > 128) {
-        // 512 rows (136 large tiles): 88 against 103 for 64 x 128; 256 rows (136 tiles
-        // of 128 x 256): 61 against 66 and 82 (68 large tiles); 2000 rows at 4096 x 4096
-        // (256 or 128): 40 against 51
+        // 512 rows (136 large tiles): 71 against 94 for 64 x 128 and 101 for 128 x 256; 256
+        // rows (136 tiles of 128 x 256): 58 against 64 (64 x 128) and 73 (68 large tiles);
+        // 2000 rows at 4096 x 4096 (256 or 128): 44 against 52
         const long long w = wgs(128, 256);
         if (w256 >= 192 || (w256 >= 128 && w > 256)) return T256x256;
         // four waves read less from LDS, eight wait less: 1024 rows at 8192 columns, K = 2048
@@ -808,7 +809,7 @@ Fp8Kernel choose(bool grouped, int E, int M, int N, int K)
     // 3000 (235 tiles of 64 x 64): 10 against 14
     if (w64 <= 128) return T64x64K2;
     if (w64 <= 256) return T64x128K2;
-    // 128 rows (136 tiles): 43 against 52; 512 rows at 17408 x 5120 (160): 115, 135
+    // 128 rows (136 tiles): 40 against 48; 512 rows at 17408 x 5120 (160): 107, 135
     if (rows > 64 && w128 <= 256) return T128x128K2;
     // (up to 128 rows an expert, many tiles)
     return T64x128;
