@@ -168,9 +168,10 @@ __device__ inline void store4(uint16_t *c, float4v x, bool zero, int n, int N, b
 // KS > 1: KS such groups of waves, each with LDS of its own, take the steps in
 // turn, and their sums meet in LDS in the order of the groups; for grids that
 // leave CUs idle or K long, where a step's latency is what counts.
-// 4096 x 5120 x 17408 (M x K x N): 332 to 348 us, 2.1 to 2.2 PFLOP/s of the 3.45 that MFMAs with four FMAs
-// each reach from registers alone; a third of the waves' time is spent at the step's
-// barrier, for loads that come from beyond L2 (with L2 hits only 10 % faster).
+// 4096 x 5120 x 17408 (M x K x N): 332 to 348 us, 2.1 to 2.2 PFLOP/s of the 3.45 that
+// MFMAs with four FMAs each reach from registers alone; a third of the waves' time is
+// spent at the step's barrier, for loads that come from beyond L2 (with L2 hits only 10 %
+// faster).
 // b: the workgroup's number among those of this tile.
 template <int BM, int BN, int WM, int WN, int KS, bool BF16>
 __device__ __forceinline__ void fp8_tile(
