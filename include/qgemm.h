@@ -100,6 +100,7 @@ extern "C" {
 #define QG_OP_W4A16_SWIGLU          5
 #define QG_OP_FP8                   6
 #define QG_OP_MOE_SORT              7  /* M = tokens, N = topk, num_experts  */
+#define QG_OP_LORA                  8  /* M = tokens, group_size = rank, num_experts = adapters */
 
 /* ---- element types, for the calls that take more than one ---- */
 #define QG_DTYPE_F16                0
@@ -433,6 +434,123 @@ int moe_sort_rows(const int32_t *ids, int T, int topk, int num_experts, int32_t 
  * 1 <= topk <= 64.  T == 0 does nothing.  One kernel, no workspace.         */
 int moe_combine_rows(const void *Y, int dtype, const int32_t *slot_row, const float *weights,
                      int T, int topk, int M_rows, int N, void *out, void *stream);
+
+/* ---- paged 4-bit key/value cache ----
+ * A cache holds, for `num_pages` pages of `page_size` tokens (a power of two
+ * from 32 to 1024), `heads` key/value heads of `head_dim` channels (64, 128 or
+ * 256) in groups of `group` channels (32, 64 or 128, at most head_dim).  A
+ * group of a token is 4-bit codes c with an fp16 scale s and an fp16 zero z
+ * (the weights' asymmetric form), and stands for c * s + z.
+ *   k, v        [num_pages, heads, page_size, head_dim/8] uint32, 16-byte aligned
+ *   k_sz, v_sz  [num_pages, heads, head_dim/group, page_size, 2] fp16 (scale,
+ *               zero), 16-byte aligned
+ * Eight codes to a word:
+ *   keys    a token's words are [4][head_dim/32]; nibble 4a + 2b + c (a, b, c 0
+ *           or 1) of word (q, 2i + l) is channel
+ *           32 (i + c head_dim/64) + 8 q + 4 l + 2 b + a.
+ *   values  the words of 32 consecutive tokens (32 n .. 32 n + 31 of a page) are
+ *           [head_dim/64][4][16][4]; nibble 4a + 2b + c of word (u, q, m, j) is
+ *           channel 64 u + 16 j + m of token 16 c + 4 q + 2 b + a.
+ * A batch is B sequences:
+ *   kv_lens     [B] int32: the tokens of each, the new ones among them.
+ *   page_table  [B, max_pages] int32: token t of sequence b is token t %
+ *               page_size of page page_table[b, t / page_size].
+ *   seq_offsets [B+1] int32, non-decreasing, or NULL (T == B): the rows
+ *               seq_offsets[b] .. seq_offsets[b+1]-1 of the call's T rows are
+ *               the LAST tokens of sequence b, in order (kv_lens[b] - n .. kv_lens[b] - 1);
+ *               NULL: row b is the last token of sequence b.  Rows outside
+ *               [seq_offsets[0], seq_offsets[B]) are left as they were.
+ * All three stand on the device and are read there.  A token whose index is
+ * negative or past the table, or whose page lies outside [0, num_pages), has no
+ * place in the cache: it is not stored, reads as zeros and is never attended
+ * to.  Two sequences may share pages that a call only reads.
+ * max_pages * page_size <= 2^30.  T == 0 or B == 0 does nothing.            */
+
+/* Keys and values of new tokens rotated, quantized and appended.
+ * k, v     rows of [heads, head_dim] fp16 or bf16 (dtype), 16-byte aligned; row t
+ *          starts ld_k (ld_v) elements after row t - 1, a multiple of 8 (so the
+ *          parts of one projection's output can be passed as they lie).
+ * q        NULL, or rows of [q_heads, head_dim] of the same type (ld_q):
+ *          rotated into q_out [T, q_heads, head_dim] (16-byte aligned, contiguous), rounded once.
+ * cos_sin  [max_pos, rot_dim] fp32, 16-byte aligned: the cosines of a position's
+ *          rot_dim / 2 angles, then the sines; NULL with rot_dim 0: no rotation.
+ *          rot_dim is a multiple of 16, at most head_dim; channels past it pass.
+ * positions  [T] int32, or NULL: each token's index in its sequence.  A position
+ *          outside [0, max_pos) makes the row's rotated channels NaN.
+ * flags    0: angle i turns the channels (i, i + rot_dim/2);
+ *          QG_KV4_INTERLEAVED: (2i, 2i + 1).
+ *            a' = a cos - b sin,  b' = b cos + a sin
+ *          in fp32, each product and each sum rounded once.
+ * A group x of a token is stored with (fp32, fp16 roundings to nearest even)
+ *            z = fp16(min x),  s = fp16((max x - min x) / 15),
+ *            c = clamp(round_half_even((x - z) / s), 0, 15),  0 where s is 0.
+ *          A group with a NaN or with values past fp16's range gets NaN scale
+ *          and zero and codes 0, and so is NaN wherever it is seen.
+ * No two rows of a call may name the same place of the cache.  One kernel, no
+ * workspace.                                                                */
+#define QG_KV4_INTERLEAVED 0x1u
+int kv4_append(const void *k, const void *v, const void *q, int dtype, int T, int ld_k, int ld_v,
+               int ld_q, int q_heads, const int32_t *seq_offsets, const int32_t *kv_lens,
+               const int32_t *page_table, int B, int max_pages, const int32_t *positions,
+               const float *cos_sin, int rot_dim, int max_pos, unsigned flags, uint32_t *cache_k,
+               uint32_t *cache_v, uint16_t *cache_k_sz, uint16_t *cache_v_sz, int num_pages,
+               int heads, int page_size, int head_dim, int group, void *q_out, void *stream);
+
+/* The rows of a batch back as values: k_out, v_out [T, heads, head_dim] of
+ * dtype QG_DTYPE_F32, _F16 or _BF16, 16-byte aligned: c * s + z in fp32, rounded once.
+ * One kernel, no workspace.                                                 */
+int kv4_read(const uint32_t *cache_k, const uint32_t *cache_v, const uint16_t *cache_k_sz,
+             const uint16_t *cache_v_sz, int num_pages, int heads, int page_size, int head_dim,
+             int group, const int32_t *seq_offsets, const int32_t *kv_lens,
+             const int32_t *page_table, int B, int max_pages, int T, int dtype, void *k_out,
+             void *v_out, void *stream);
+
+/* Attention of new tokens over the cache (which holds them already).
+ * q        rows of [q_heads, head_dim] fp16 or bf16, 16-byte aligned, ld_q as
+ *          above; q_heads a multiple of heads: query head j reads key/value
+ *          head j / (q_heads / heads).
+ * out      [T, q_heads, head_dim] of q's type, 16-byte aligned:
+ *            out = sum_t p_t V_t,  p = softmax over the visible t of scale * q . K_t
+ *          A token at position i (its index in the sequence) sees t <= i, and
+ *          with window > 0 only t > i - window or t < sinks (the first tokens
+ *          stay visible).  A row that sees nothing gets zeros.
+ * scale    finite and > 0.
+ * max_new  the expected largest number of rows of a sequence: it only picks the
+ *          kernel, so a wrong one is slower, never wrong.
+ * Scores, the softmax's maximum and sum and the accumulators are fp32; the
+ * queries and codes enter the products exactly (a query's channels down to
+ * 2^-24 of its largest), p_t * s_t rounded to fp16 once.  Results depend on the
+ * arguments' sizes, not on timing.
+ * workspace  kv4_attend_workspace_bytes(...) bytes, 256-byte aligned (NULL when
+ *          0); nothing is kept in it between calls.  One or two kernels.     */
+size_t kv4_attend_workspace_bytes(int T, int max_new, int B, int q_heads, int heads, int head_dim,
+                                  int max_pages, int page_size, int window, int sinks);
+int kv4_attend(const void *q, int dtype, int T, int ld_q, int q_heads, int max_new,
+               const int32_t *seq_offsets, const int32_t *kv_lens, const int32_t *page_table, int B,
+               int max_pages, const uint32_t *cache_k, const uint32_t *cache_v,
+               const uint16_t *cache_k_sz, const uint16_t *cache_v_sz, int num_pages, int heads,
+               int page_size, int head_dim, int group, float scale, int window, int sinks,
+               void *out, void *workspace, size_t workspace_bytes, unsigned flags, void *stream);
+
+/* ---- low-rank adapters of many requests beside a shared projection ----
+ *   Y[t] += scaling[a] * (X[t] . A[a]^T) . B[a]^T     for the tokens t of adapter a
+ * X        [T,K], A [L,R,K], B [L,N,R], Y [T,N] (read and written), all fp16 or
+ *          all bf16 (dtype), 16-byte aligned; K, N, R multiples of 8, R <= 512.
+ * scaling  [L] fp32, or NULL for ones.
+ * adapter_offsets [L+1], row_token [T], slot_row [T]: moe_sort_rows of the
+ *          tokens' adapters (topk = 1, ids outside [0, L) for tokens without
+ *          one): row m of adapter a's range is token row_token[m], if
+ *          slot_row[row_token[m]] is m.  Tokens without a row keep their Y.
+ * Both products and their sum with Y in fp32 (X . A^T enters the second as a sum
+ * of two 16-bit values: 22 bits of a row's largest for fp16, 16 for bf16), one rounding to Y's
+ * type.  Y must not overlap the other tensors.
+ * workspace  qg_workspace_bytes(QG_OP_LORA, T, N, K, R, L, 0) bytes, 256-byte
+ *          aligned; nothing is kept in it between calls.  T == 0 does nothing.
+ *          Two kernels.                                                      */
+int lora_add(const void *X, const void *A, const void *B, const float *scaling,
+             const int32_t *adapter_offsets, const int32_t *row_token, const int32_t *slot_row,
+             int L, int T, int K, int N, int R, int dtype, void *Y, void *workspace,
+             size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -13,6 +13,9 @@ quantize_rows_fp8, qgemm_fp8, moe_route, moe_sort_rows, moe_combine_rows (plus
 qg_device_supported, qg_workspace_bytes, qg_padded_shape); pack, w4a16,
 w4a16_swiglu, correct, quantize_rows, w4a8, quantize_fp8, fp8_gemm, route,
 sort_rows and combine_rows are the same calls with torch-allocated outputs.
+The paged 4-bit cache (KV4Cache, kv4_cache, kv4_append, kv4_read, kv4_attend) and
+the adapters (lora) take the arguments of kv4_append, kv4_read, kv4_attend and
+lora_add from their tensors' shapes.
 """
 import ctypes
 import functools
@@ -46,6 +49,7 @@ QG_OP_PACK = 4
 QG_OP_W4A16_SWIGLU = 5
 QG_OP_FP8 = 6
 QG_OP_MOE_SORT = 7
+QG_OP_LORA = 8
 
 QG_DTYPE_F16 = 0
 QG_DTYPE_BF16 = 1
@@ -55,12 +59,14 @@ QG_QUANT_SWIGLU = 0x1
 QG_ROUTE_SIGMOID = 0x1
 QG_ROUTE_RENORMALIZE = 0x2
 QG_ROUTE_GROUP_TOP2 = 0x4
+QG_KV4_INTERLEAVED = 0x1
 
 EXPORTED = ("qg_device_supported", "qg_status_string", "qg_last_error", "qg_workspace_bytes",
             "pack_int4_weights", "qgemm_w4a16", "group_sum_correction", "qgemm_w4a8",
             "quantize_rows_int8", "qgemm_w4a16_swiglu", "qg_padded_shape",
             "qgemm_w4a16_noalloc", "quantize_rows_fp8", "qgemm_fp8", "moe_route", "moe_sort_rows",
-            "moe_combine_rows")
+            "moe_combine_rows", "kv4_append", "kv4_read", "kv4_attend_workspace_bytes", "kv4_attend",
+            "lora_add")
 
 
 class QGemmError(RuntimeError):
@@ -132,6 +138,17 @@ def open_library(path):
     L.moe_sort_rows.argtypes = [P, I, I, I, P, P, P, P, Z, P]
     L.moe_combine_rows.restype = I
     L.moe_combine_rows.argtypes = [P, I, P, P, I, I, I, I, P, P]
+    batch, cache = [P, P, P, I, I], [P, P, P, P, I, I, I, I, I]
+    L.kv4_append.restype = I
+    L.kv4_append.argtypes = [P, P, P, I, I, I, I, I, I] + batch + [P, P, I, I, U] + cache + [P, P]
+    L.kv4_read.restype = I
+    L.kv4_read.argtypes = cache + batch + [I, I, P, P, P]
+    L.kv4_attend_workspace_bytes.restype = Z
+    L.kv4_attend_workspace_bytes.argtypes = [I] * 10
+    L.kv4_attend.restype = I
+    L.kv4_attend.argtypes = [P, I, I, I, I, I] + batch + cache + [ctypes.c_float, I, I, P, P, Z, U, P]
+    L.lora_add.restype = I
+    L.lora_add.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, P, P, Z, P]
     return L
 
 
@@ -630,3 +647,245 @@ def combine_rows(Y: torch.Tensor, slot_row: torch.Tensor, weights: torch.Tensor,
         out = torch.empty((T, N), dtype=Y.dtype, device=Y.device)
     moe_combine_rows(Y, slot_row, weights, T, topk, M_rows, N, out)
     return out
+
+
+# ---- paged 4-bit key/value cache, low-rank adapters ----
+# Workspaces come from torch's allocator on each call: nothing is kept in them, and calls
+# on other streams or in graphs captured side by side get their own.
+
+@dataclass
+class KV4Cache:
+    """A paged 4-bit key/value cache (layout in include/qgemm.h)."""
+    k: torch.Tensor       # int32 [pages, heads, page_size, head_dim/8] (uint32 bit patterns)
+    v: torch.Tensor       # the same
+    k_sz: torch.Tensor    # fp16 [pages, heads, head_dim/group, page_size, 2]: scale and zero
+    v_sz: torch.Tensor    # the same
+
+    @property
+    def pages(self) -> int:
+        return self.k.shape[0]
+
+    @property
+    def heads(self) -> int:
+        return self.k.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.k.shape[2]
+
+    @property
+    def head_dim(self) -> int:
+        return 8 * self.k.shape[3]
+
+    @property
+    def group(self) -> int:
+        return self.head_dim // max(self.k_sz.shape[2], 1)
+
+
+def kv4_cache(pages: int, heads: int, head_dim: int, page_size: int = 64, group: int = 64,
+              device="cuda") -> KV4Cache:
+    """An empty cache: every token's codes, scales and zeros 0."""
+    if head_dim not in (64, 128, 256) or group not in (32, 64, 128) or group > head_dim:
+        raise ValueError(f"head_dim {head_dim} in groups of {group}: head_dim must be 64, 128 or 256, group 32, 64 or "
+                         "128 and at most head_dim")
+    if page_size not in (32, 64, 128, 256, 512, 1024):
+        raise ValueError(f"page_size must be a power of two from 32 to 1024, got {page_size}")
+    words = lambda: torch.zeros((pages, heads, page_size, head_dim // 8), dtype=torch.int32, device=device)  # noqa: E731
+    sz = lambda: torch.zeros((pages, heads, head_dim // group, page_size, 2), dtype=torch.float16, device=device)  # noqa: E731
+    return KV4Cache(k=words(), v=words(), k_sz=sz(), v_sz=sz())
+
+
+def _kv4_cache_args(c: KV4Cache, dev):
+    """The C entry points' arguments of a cache."""
+    k, sz = c.k, c.k_sz
+    if not isinstance(k, torch.Tensor) or not isinstance(sz, torch.Tensor) or k.dim() != 4 or sz.dim() != 5:
+        raise ValueError("a cache's k is [pages, heads, page_size, head_dim/8], its k_sz [pages, heads, "
+                         "head_dim/group, page_size, 2]")
+    shape = tuple(k.shape)
+    pages, heads, page, d8 = shape
+    groups = sz.shape[2]
+    if groups < 1 or 8 * d8 % groups:
+        raise ValueError(f"head_dim {8 * d8} in {groups} groups")
+    if (pages | heads | page | d8) >> 28:
+        _too_many(*shape)
+    sz_shape = (pages, heads, groups, page, 2)
+    return (_arg(k, torch.int32, shape, dev, "cache.k"), _arg(c.v, torch.int32, shape, dev, "cache.v"),
+            _arg(sz, torch.float16, sz_shape, dev, "cache.k_sz"),
+            _arg(c.v_sz, torch.float16, sz_shape, dev, "cache.v_sz"), pages, heads, page, 8 * d8, 8 * d8 // groups)
+
+
+def _kv4_batch_args(T, seq_offsets, kv_lens, page_table, dev):
+    """The C entry points' arguments of a batch."""
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table is [B, max_pages]")
+    B, width = page_table.shape
+    if (T | B | width) >> 31:
+        _too_many(T, B, width)
+    return (_arg(seq_offsets, torch.int32, (B + 1,), dev, "seq_offsets"), _arg(kv_lens, torch.int32, (B,), dev, "kv_lens"),
+            _arg(page_table, torch.int32, (B, width), dev, "page_table"), B, width)
+
+
+def _kv4_rows(t: torch.Tensor, dtype, T, heads, D, dev, name):
+    """The pointer of rows [T, heads, D], each row's heads together, and the elements from
+    one row to the next."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (T, heads, D):
+        raise ValueError(f"{name} must be {[T, heads, D]}, got {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on GPU {dev}")
+    ld, per_head, one = t.stride()
+    if one != 1 or (heads > 1 and per_head != D):
+        raise ValueError(f"the heads of a row of {name} must stand together (strides {t.stride()})")
+    if T <= 1:
+        ld = heads * D
+    if ld >> 31:
+        raise ValueError(f"rows of {name} {ld} elements apart")
+    return t.data_ptr(), ld
+
+
+def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor,
+               seq_offsets: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+               cos_sin: Optional[torch.Tensor] = None, interleaved: bool = False,
+               q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None):
+    """Append rows [T, heads, head_dim] of keys (rotated by cos_sin [positions, rot_dim], if
+    given) and values to the cache, as the last tokens of the sequences whose lengths
+    kv_lens gives (the new tokens among them); see include/qgemm.h.  The rows may be
+    parts of a wider tensor.  Returns the rotated q (a new tensor, or q_out), None without q."""
+    d = _dtype(k, "k")
+    dev, T, D = k.get_device(), k.shape[0], cache.head_dim
+    cargs = _kv4_cache_args(cache, dev)
+    batch = _kv4_batch_args(T, seq_offsets, kv_lens, page_table, dev)
+    heads = cargs[5]
+    kp, ldk = _kv4_rows(k, k.dtype, T, heads, D, dev, "k")
+    vp, ldv = _kv4_rows(v, k.dtype, T, heads, D, dev, "v")
+    qp = op = None
+    ldq = q_heads = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError(f"q must be [T, q_heads, {D}]")
+        q_heads = q.shape[1]
+        qp, ldq = _kv4_rows(q, k.dtype, T, q_heads, D, dev, "q")
+        if q_out is None:
+            q_out = torch.empty((T, q_heads, D), dtype=q.dtype, device=q.device)
+        op = _arg(q_out, k.dtype, (T, q_heads, D), dev, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = max_pos = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin is [positions, rot_dim]")
+        max_pos, rot = cos_sin.shape
+        if max_pos >> 31:
+            _too_many(max_pos)
+        if rot == 0:
+            raise ValueError("cos_sin without angles")
+    _call(lib().kv4_append, dev, kp, vp, qp, d, T, ldk, ldv, ldq, q_heads, *batch,
+          _arg(positions, torch.int32, (T,), dev, "positions"),
+          _arg(cos_sin, torch.float32, (max_pos, rot), dev, "cos_sin"), rot, max_pos,
+          QG_KV4_INTERLEAVED if interleaved else 0, *cargs, op)
+    return q_out
+
+
+def kv4_read(cache: KV4Cache, kv_lens: torch.Tensor, page_table: torch.Tensor,
+             seq_offsets: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+             v_out: Optional[torch.Tensor] = None, rows: Optional[int] = None, dtype: torch.dtype = torch.bfloat16):
+    """The last rows of each sequence (as many as seq_offsets gives each, one without it) back from the cache as
+    values: (keys, values) [T, heads, head_dim].  `rows` is T where seq_offsets is given and
+    k_out is not."""
+    dev = page_table.get_device()
+    cargs = _kv4_cache_args(cache, dev)
+    heads, D = cargs[5], cargs[7]
+    if k_out is not None:
+        T, dtype = k_out.shape[0], k_out.dtype
+    elif rows is not None or seq_offsets is not None:
+        if rows is None:
+            raise ValueError("rows (the number of rows that seq_offsets ends with) is needed without k_out")
+        T = rows
+    else:
+        T = page_table.shape[0]
+    if dtype not in _DTYPES:
+        raise TypeError("dtype must be fp32, fp16 or bf16")
+    if T < 0:
+        raise ValueError(f"rows must be >= 0, got {T}")
+    shape = (T, heads, D)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=page_table.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=page_table.device)
+    _call(lib().kv4_read, dev, *cargs, *_kv4_batch_args(T, seq_offsets, kv_lens, page_table, dev), T, _DTYPES[dtype],
+          _arg(k_out, dtype, shape, dev, "k_out"), _arg(v_out, dtype, shape, dev, "v_out"))
+    return k_out, v_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _attend_workspace(*args):
+    n = lib().kv4_attend_workspace_bytes(*args)
+    if n == ctypes.c_size_t(-1).value:
+        raise QGemmError(QG_ERR_INVALID_ARG, lib().qg_last_error().decode())
+    return int(n)
+
+
+def kv4_attend(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, page_table: torch.Tensor,
+               seq_offsets: Optional[torch.Tensor] = None, max_new: Optional[int] = None,
+               scale: Optional[float] = None, window: int = 0, sinks: int = 0,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Causal attention of the sequences' last tokens (q [T, q_heads, head_dim], one row a sequence
+    or seq_offsets' ragged runs) over the cache that holds them; window > 0: each token
+    sees that many, itself among them, and the first `sinks`.  max_new: the expected largest
+    number of rows of a sequence (default: T with seq_offsets)."""
+    d = _dtype(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [T, q_heads, head_dim]")
+    dev = q.get_device()
+    cargs = _kv4_cache_args(cache, dev)
+    heads, page, D = cargs[5:8]
+    T, q_heads = q.shape[0], q.shape[1]
+    batch = _kv4_batch_args(T, seq_offsets, kv_lens, page_table, dev)
+    qp, ldq = _kv4_rows(q, q.dtype, T, q_heads, D, dev, "q")
+    if max_new is None:
+        max_new = 1 if seq_offsets is None else max(T, 1)
+    for n in (max_new, window, sinks):
+        if not 0 <= n < 1 << 31:
+            raise ValueError(f"max_new, window and sinks {(max_new, window, sinks)} must lie in 0 .. 2^31 - 1")
+    if out is None:
+        out = torch.empty((T, q_heads, D), dtype=q.dtype, device=q.device)
+    n = _attend_workspace(T, max_new, batch[3], q_heads, heads, D, batch[4], page, window, sinks)
+    ws = torch.empty(n, dtype=torch.uint8, device=q.device) if n > 0 else None
+    _call(lib().kv4_attend, dev, qp, d, T, ldq, q_heads, max_new, *batch, *cargs,
+          D ** -0.5 if scale is None else scale, window, sinks, _arg(out, q.dtype, (T, q_heads, D), dev, "out"),
+          *_scratch(ws, dev), 0)
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _lora_workspace(T, N, K, R, L):
+    return qg_workspace_bytes(QG_OP_LORA, T, N, K, R, L, 0)
+
+
+def lora(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, plan, y: torch.Tensor,
+         scaling: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[t] += scaling[a] * (x[t] . A[a]^T) . B[a]^T in place for the tokens t of each adapter a:
+    x [T,K], A [L,R,K], B [L,N,R], y [T,N] of one 16-bit type.  plan: sort_rows of the tokens'
+    adapters as [T,1] ids (negative: none), made once for all projections of a batch."""
+    d = _dtype(x, "x")
+    offsets, rows, slots = plan
+    if x.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("x is [T,K], A [L,R,K], B [L,N,R]")
+    T, K = x.shape
+    L, R, N = A.shape[0], A.shape[1], B.shape[1]
+    if (T | K | L | R | N) >> 31:
+        _too_many(T, K, L, R, N)
+    dev = x.get_device()
+    args = (_arg(x, None, (T, K), dev, "x"), _arg(A, x.dtype, (L, R, K), dev, "A"), _arg(B, x.dtype, (L, N, R), dev, "B"),
+            _arg(scaling, torch.float32, (L,), dev, "scaling"), _arg(offsets, torch.int32, (L + 1,), dev, "plan's offsets"),
+            _arg(rows, torch.int32, (T,), dev, "plan's rows"), _arg(slots, torch.int32, (T, 1), dev, "plan's slots"),
+            L, T, K, N, R, d, _arg(y, x.dtype, (T, N), dev, "y"))
+    n = _lora_workspace(T, N, K, R, L)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n > 0 else None
+    _call(lib().lora_add, dev, *args, *_scratch(ws, dev))
+    return y

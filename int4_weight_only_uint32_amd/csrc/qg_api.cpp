@@ -12,6 +12,7 @@
 #include <set>
 #include <string>
 
+#include "qg_kv4.h"
 #include "qg_launch.h"
 
 namespace {
@@ -270,6 +271,75 @@ int check_sort_shape(const char *what, int T, int topk, int E)
     return QG_OK;
 }
 
+// Cache and batch of the kv4 calls; *c and *s as the kernels take them.
+int check_kv4(const char *what, const void *k, const void *v, const void *k_sz, const void *v_sz, int pages, int heads,
+              int page_size, int D, int g, const int32_t *off, const int32_t *lens, const int32_t *table, int B,
+              int max_pages, int T, qg::Kv4Cache *c, qg::Kv4Batch *s)
+{
+    if (pages < 1 || heads < 1 || max_pages < 1 || B < 0 || T < 0)
+        return fail(QG_ERR_INVALID_ARG, "%s: num_pages=%d, heads=%d, max_pages=%d, B=%d, T=%d", what, pages, heads,
+                    max_pages, B, T);
+    if (D != 64 && D != 128 && D != 256)
+        return fail(QG_ERR_UNSUPPORTED, "%s: head_dim must be 64, 128 or 256 (got %d)", what, D);
+    if ((g != 32 && g != 64 && g != 128) || g > D)
+        return fail(QG_ERR_UNSUPPORTED, "%s: group must be 32, 64 or 128 and at most head_dim=%d (got %d)", what, D, g);
+    if (page_size < 32 || page_size > 1024 || (page_size & (page_size - 1)))
+        return fail(QG_ERR_UNSUPPORTED, "%s: page_size must be a power of two from 32 to 1024 (got %d)", what, page_size);
+    if (heads > 4096 || (long long)max_pages * page_size > (1ll << 30) || T >= (1 << 28) || B >= (1 << 28) ||
+        (long long)pages * heads > 0x7FFFFFFFll)
+        return fail(QG_ERR_UNSUPPORTED, "%s: heads=%d, max_pages=%d, num_pages=%d, T=%d, B=%d too large", what, heads,
+                    max_pages, pages, T, B);
+    if (!off && T != B)
+        return fail(QG_ERR_INVALID_ARG, "%s: T=%d rows of B=%d sequences need seq_offsets", what, T, B);
+    if (T > 0 && B > 0) {
+        if (!k || !v || !k_sz || !v_sz) return fail(QG_ERR_INVALID_ARG, "%s: NULL cache", what);
+        if (!lens || !table) return fail(QG_ERR_INVALID_ARG, "%s: NULL kv_lens/page_table", what);
+        if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_sz, 16) || !aligned(v_sz, 16) || !aligned(lens, 4) ||
+            !aligned(table, 4) || (off && !aligned(off, 4)))
+            return fail(QG_ERR_INVALID_ARG, "%s: misaligned cache, lengths, offsets or page table", what);
+    }
+    *c = qg::Kv4Cache{(uint32_t *)k, (uint32_t *)v, (uint32_t *)k_sz, (uint32_t *)v_sz, pages, heads,
+                      __builtin_ctz((unsigned)page_size), D, g};
+    *s = qg::Kv4Batch{off, lens, table, B, max_pages, T};
+    return QG_OK;
+}
+
+// Rows of `heads` heads of D channels, ld elements apart.
+int check_kv4_rows(const char *what, const char *name, const void *p, int ld, int heads, int D)
+{
+    if (!p) return fail(QG_ERR_INVALID_ARG, "%s: NULL %s", what, name);
+    if (!aligned(p, 16)) return fail(QG_ERR_INVALID_ARG, "%s: misaligned %s", what, name);
+    if (ld % 8 || ld < (long long)heads * D)
+        return fail(QG_ERR_INVALID_ARG, "%s: rows of %s %d elements apart (a multiple of 8, at least %lld)", what, name,
+                    ld, (long long)heads * D);
+    return QG_OK;
+}
+
+int check_attend_shape(const char *what, int T, int max_new, int B, int q_heads, int heads, int window, int sinks)
+{
+    if (max_new < 1 || window < 0 || sinks < 0)
+        return fail(QG_ERR_INVALID_ARG, "%s: max_new=%d, window=%d, sinks=%d", what, max_new, window, sinks);
+    if (heads < 1 || q_heads < 1 || q_heads % heads)
+        return fail(QG_ERR_INVALID_ARG, "%s: %d query heads over %d key/value heads", what, q_heads, heads);
+    if ((long long)T * q_heads >= (1ll << 30) || (long long)B * q_heads >= (1ll << 30))
+        return fail(QG_ERR_UNSUPPORTED, "%s: T=%d, B=%d, q_heads=%d too large", what, T, B, q_heads);
+    return QG_OK;
+}
+
+// Window and sinks past every token are none and all.
+int capped(int n) { return n < (1 << 30) ? n : 1 << 30; }
+
+int check_lora_shape(const char *what, int T, int L, int K, int N, int R)
+{
+    if (T < 0 || L < 1 || K < 1 || N < 1 || R < 1)
+        return fail(QG_ERR_INVALID_ARG, "%s: T >= 0, L, K, N, R >= 1 needed (got %d, %d, %d, %d, %d)", what, T, L, K, N, R);
+    if (K % 8 || N % 8 || R % 8)
+        return fail(QG_ERR_UNSUPPORTED, "%s: K, N, R must be multiples of 8 (got %d, %d, %d)", what, K, N, R);
+    if (L > 65535 || R > 512 || K > (1 << 24) || N > (1 << 24) || T >= (1 << 24))
+        return fail(QG_ERR_UNSUPPORTED, "%s: T=%d, L=%d, K=%d, N=%d, R=%d too large", what, T, L, K, N, R);
+    return QG_OK;
+}
+
 } // namespace
 
 extern "C" {
@@ -355,6 +425,9 @@ size_t qg_workspace_bytes(int op, int M, int N, int K, int group_size, int num_e
     case QG_OP_MOE_SORT:
         if (check_sort_shape("qg_workspace_bytes", M, N, num_experts) != QG_OK) return (size_t)-1;
         return qg::moe_sort_workspace_bytes(M, N, num_experts);
+    case QG_OP_LORA:
+        if (check_lora_shape("qg_workspace_bytes", M, num_experts, K, N, group_size) != QG_OK) return (size_t)-1;
+        return M == 0 ? 0 : qg::lora_plan(M, num_experts, K, N, group_size).bytes;
     case QG_OP_PACK:
         if (check_shape("qg_workspace_bytes", M < 1 ? 1 : M, N, K, &g) != QG_OK) return (size_t)-1;
         return 0;
@@ -734,6 +807,158 @@ int moe_combine_rows(const void *Y, int dtype, const int32_t *slot_row, const fl
                                               (hipStream_t)stream),
                        what, (hipStream_t)stream);
     if (rc == QG_OK) log_first("%s T=%d topk=%d N=%d", what, T, topk, N);
+    return rc;
+}
+
+int kv4_append(const void *k, const void *v, const void *q, int dtype, int T, int ld_k, int ld_v, int ld_q, int q_heads,
+               const int32_t *seq_offsets, const int32_t *kv_lens, const int32_t *page_table, int B, int max_pages,
+               const int32_t *positions, const float *cos_sin, int rot_dim, int max_pos, unsigned flags,
+               uint32_t *cache_k, uint32_t *cache_v, uint16_t *cache_k_sz, uint16_t *cache_v_sz, int num_pages,
+               int heads, int page_size, int head_dim, int group, void *q_out, void *stream)
+{
+    const char *const what = "kv4_append";
+    qg::Kv4Cache c;
+    qg::Kv4Batch s;
+    int rc = check_kv4(what, cache_k, cache_v, cache_k_sz, cache_v_sz, num_pages, heads, page_size, head_dim, group,
+                       seq_offsets, kv_lens, page_table, B, max_pages, T, &c, &s);
+    if (rc) return rc;
+    if ((rc = check_dtype16(what, dtype))) return rc;
+    if (flags & ~QG_KV4_INTERLEAVED) return fail(QG_ERR_INVALID_ARG, "%s: unknown flags 0x%x", what, flags);
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16)
+        return fail(QG_ERR_UNSUPPORTED, "%s: rot_dim must be a multiple of 16, at most head_dim=%d (got %d)", what,
+                    head_dim, rot_dim);
+    if (rot_dim > 0 && (!cos_sin || max_pos < 1 || !aligned(cos_sin, 16)))
+        return fail(QG_ERR_INVALID_ARG, "%s: rot_dim=%d without angles (16-byte aligned, max_pos >= 1)", what, rot_dim);
+    if (q && (q_heads < 1 || q_heads > (1 << 18)))
+        return fail(QG_ERR_INVALID_ARG, "%s: q_heads=%d out of range", what, q_heads);
+    if (T == 0 || B == 0) return ok();
+    if ((rc = check_kv4_rows(what, "k", k, ld_k, heads, head_dim))) return rc;
+    if ((rc = check_kv4_rows(what, "v", v, ld_v, heads, head_dim))) return rc;
+    if (q && (rc = check_kv4_rows(what, "q", q, ld_q, q_heads, head_dim))) return rc;
+    if (q && (!q_out || !aligned(q_out, 16))) return fail(QG_ERR_INVALID_ARG, "%s: NULL or misaligned q_out", what);
+    if (positions && !aligned(positions, 4)) return fail(QG_ERR_INVALID_ARG, "%s: misaligned positions", what);
+    if (qg::kv4_blocks_bound(T, B) * 256 > MAX_GRID_THREADS)
+        return fail(QG_ERR_UNSUPPORTED, "%s: T=%d, B=%d too large for one launch", what, T, B);
+    if ((rc = check_device())) return rc;
+    rc = launch_status(qg::launch_kv4_append(c, s, k, v, q, ld_k, ld_v, ld_q, q_heads, dtype, positions, cos_sin, rot_dim,
+                                             max_pos, (flags & QG_KV4_INTERLEAVED) != 0, q_out, (hipStream_t)stream),
+                       what, (hipStream_t)stream);
+    if (rc == QG_OK)
+        log_first("%s T=%d B=%d heads=%d head_dim=%d group=%d page_size=%d rot_dim=%d%s %s%s", what, T, B, heads, head_dim,
+                  group, page_size, rot_dim, (flags & QG_KV4_INTERLEAVED) ? " interleaved" : "",
+                  dtype == QG_DTYPE_BF16 ? "bf16" : "fp16", q ? ", queries" : "");
+    return rc;
+}
+
+int kv4_read(const uint32_t *cache_k, const uint32_t *cache_v, const uint16_t *cache_k_sz, const uint16_t *cache_v_sz,
+             int num_pages, int heads, int page_size, int head_dim, int group, const int32_t *seq_offsets,
+             const int32_t *kv_lens, const int32_t *page_table, int B, int max_pages, int T, int dtype, void *k_out,
+             void *v_out, void *stream)
+{
+    const char *const what = "kv4_read";
+    qg::Kv4Cache c;
+    qg::Kv4Batch s;
+    int rc = check_kv4(what, cache_k, cache_v, cache_k_sz, cache_v_sz, num_pages, heads, page_size, head_dim, group,
+                       seq_offsets, kv_lens, page_table, B, max_pages, T, &c, &s);
+    if (rc) return rc;
+    if (dtype != QG_DTYPE_F32 && dtype != QG_DTYPE_F16 && dtype != QG_DTYPE_BF16)
+        return fail(QG_ERR_INVALID_ARG, "%s: unknown dtype %d", what, dtype);
+    if (T == 0 || B == 0) return ok();
+    if (!k_out || !v_out) return fail(QG_ERR_INVALID_ARG, "%s: NULL k_out/v_out", what);
+    if (!aligned(k_out, 16) || !aligned(v_out, 16)) return fail(QG_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+    if (qg::kv4_blocks_bound(T, B) * 256 > MAX_GRID_THREADS)
+        return fail(QG_ERR_UNSUPPORTED, "%s: T=%d, B=%d too large for one launch", what, T, B);
+    if ((rc = check_device())) return rc;
+    rc = launch_status(qg::launch_kv4_read(c, s, dtype, k_out, v_out, (hipStream_t)stream), what, (hipStream_t)stream);
+    if (rc == QG_OK)
+        log_first("%s T=%d B=%d heads=%d head_dim=%d group=%d page_size=%d", what, T, B, heads, head_dim, group, page_size);
+    return rc;
+}
+
+size_t kv4_attend_workspace_bytes(int T, int max_new, int B, int q_heads, int heads, int head_dim, int max_pages,
+                                  int page_size, int window, int sinks)
+{
+    const char *const what = "kv4_attend_workspace_bytes";
+    if (T < 0 || B < 0 || max_pages < 1 || page_size < 1 || head_dim < 1 ||
+        (long long)max_pages * page_size > (1ll << 30)) {
+        fail(QG_ERR_INVALID_ARG, "%s: T=%d, B=%d, head_dim=%d, max_pages=%d, page_size=%d", what, T, B, head_dim,
+             max_pages, page_size);
+        return (size_t)-1;
+    }
+    if (check_attend_shape(what, T, max_new, B, q_heads, heads, window, sinks) != QG_OK) return (size_t)-1;
+    if (T == 0 || B == 0) return 0;
+    return qg::kv4_attend_plan(T, max_new, B, q_heads, heads, head_dim, max_pages * page_size, capped(window),
+                               capped(sinks)).bytes;
+}
+
+int kv4_attend(const void *q, int dtype, int T, int ld_q, int q_heads, int max_new, const int32_t *seq_offsets,
+               const int32_t *kv_lens, const int32_t *page_table, int B, int max_pages, const uint32_t *cache_k,
+               const uint32_t *cache_v, const uint16_t *cache_k_sz, const uint16_t *cache_v_sz, int num_pages, int heads,
+               int page_size, int head_dim, int group, float scale, int window, int sinks, void *out, void *workspace,
+               size_t workspace_bytes, unsigned flags, void *stream)
+{
+    const char *const what = "kv4_attend";
+    qg::Kv4Cache c;
+    qg::Kv4Batch s;
+    int rc = check_kv4(what, cache_k, cache_v, cache_k_sz, cache_v_sz, num_pages, heads, page_size, head_dim, group,
+                       seq_offsets, kv_lens, page_table, B, max_pages, T, &c, &s);
+    if (rc) return rc;
+    if ((rc = check_dtype16(what, dtype))) return rc;
+    if ((rc = check_attend_shape(what, T, max_new, B, q_heads, heads, window, sinks))) return rc;
+    if (!(scale > 0.0f) || scale > 3.0e38f) return fail(QG_ERR_INVALID_ARG, "%s: scale must be finite and > 0", what);
+    if (flags != 0) return fail(QG_ERR_INVALID_ARG, "%s: unknown flags 0x%x", what, flags);
+    if (T == 0 || B == 0) return ok();
+    if ((rc = check_kv4_rows(what, "q", q, ld_q, q_heads, head_dim))) return rc;
+    if (!out || !aligned(out, 16)) return fail(QG_ERR_INVALID_ARG, "%s: NULL or misaligned out", what);
+    const qg::Kv4AttendPlan plan = qg::kv4_attend_plan(T, max_new, B, q_heads, heads, head_dim, max_pages * page_size,
+                                                       capped(window), capped(sinks));
+    if (plan.workgroups * 256 > MAX_GRID_THREADS)
+        return fail(QG_ERR_UNSUPPORTED, "%s: T=%d, B=%d, q_heads=%d too large for one launch", what, T, B, q_heads);
+    if (plan.bytes > 0) {
+        if (!workspace || workspace_bytes < plan.bytes)
+            return fail(QG_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, got %zu", what, plan.bytes,
+                        workspace ? workspace_bytes : (size_t)0);
+        if (!aligned(workspace, 256))
+            return fail(QG_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", what);
+    }
+    if ((rc = check_device())) return rc;
+    rc = launch_status(qg::launch_kv4_attend(plan, c, s, q, ld_q, q_heads, dtype, scale, capped(window), capped(sinks),
+                                             out, plan.bytes ? workspace : nullptr, (hipStream_t)stream),
+                       what, (hipStream_t)stream);
+    if (rc == QG_OK)
+        log_first("%s T=%d B=%d max_new=%d heads=%d/%d head_dim=%d group=%d page_size=%d window=%d sinks=%d %s: %d rows a "
+                  "wave, %d parts", what, T, B, max_new, q_heads, heads, head_dim, group, page_size, window, sinks,
+                  dtype == QG_DTYPE_BF16 ? "bf16" : "fp16", plan.rows, plan.splits);
+    return rc;
+}
+
+int lora_add(const void *X, const void *A, const void *B, const float *scaling, const int32_t *adapter_offsets,
+             const int32_t *row_token, const int32_t *slot_row, int L, int T, int K, int N, int R, int dtype, void *Y,
+             void *workspace, size_t workspace_bytes, void *stream)
+{
+    const char *const what = "lora_add";
+    int rc = check_dtype16(what, dtype);
+    if (rc) return rc;
+    if ((rc = check_lora_shape(what, T, L, K, N, R))) return rc;
+    if (T == 0) return ok();
+    if (!X || !A || !B || !Y || !adapter_offsets || !row_token || !slot_row)
+        return fail(QG_ERR_INVALID_ARG, "%s: NULL X/A/B/Y/adapter_offsets/row_token/slot_row", what);
+    if (!aligned(X, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(Y, 16) || (scaling && !aligned(scaling, 4)) ||
+        !aligned(adapter_offsets, 4) || !aligned(row_token, 4) || !aligned(slot_row, 4))
+        return fail(QG_ERR_INVALID_ARG, "%s: misaligned pointer", what);
+    const qg::LoraPlan plan = qg::lora_plan(T, L, K, N, R);
+    if (plan.tiles * 256 > MAX_GRID_THREADS) return fail(QG_ERR_UNSUPPORTED, "%s: T=%d too large for one launch", what, T);
+    if (!workspace || workspace_bytes < plan.bytes)
+        return fail(QG_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, got %zu", what, plan.bytes,
+                    workspace ? workspace_bytes : (size_t)0);
+    if (!aligned(workspace, 256)) return fail(QG_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", what);
+    if ((rc = check_device())) return rc;
+    rc = launch_status(qg::launch_lora(plan, X, A, B, scaling, adapter_offsets, row_token, slot_row, L, T, K, N, R, dtype,
+                                       Y, workspace, (hipStream_t)stream),
+                       what, (hipStream_t)stream);
+    if (rc == QG_OK)
+        log_first("%s T=%d L=%d K=%d N=%d R=%d %s: %d-row tiles, K in %d parts", what, T, L, K, N, R,
+                  dtype == QG_DTYPE_BF16 ? "bf16" : "fp16", 16 * plan.mt, plan.splits);
     return rc;
 }
 

@@ -169,4 +169,42 @@ hipError_t launch_moe_combine(const void *Y, int dtype, const int32_t *slot_row,
                               const float *weights, int T, int topk, int M_rows, int N, void *out,
                               hipStream_t st);
 
+// ---- paged 4-bit key/value cache (qg_kv4.h) ----
+struct Kv4Cache;
+struct Kv4Batch;
+// Upper bound of the 32-token blocks that T new rows of B sequences lie in.
+long long kv4_blocks_bound(int T, int B);
+// ld*: elements from one token's row to the next; q may be nullptr.
+hipError_t launch_kv4_append(const Kv4Cache &c, const Kv4Batch &s, const void *k, const void *v, const void *q,
+                             long long ldk, long long ldv, long long ldq, int q_heads, int dtype,
+                             const int32_t *positions, const float *cos_sin, int rot, int max_pos, bool inter,
+                             void *q_out, hipStream_t st);
+hipError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &s, int dtype, void *k_out, void *v_out, hipStream_t st);
+// How an attention call is cut: whether a workgroup's waves share their rows, rows of
+// a wave, parts along the tokens, workgroups, bytes of workspace.
+struct Kv4AttendPlan {
+    bool shared;
+    int rows, splits;
+    long long workgroups;
+    size_t bytes;
+};
+Kv4AttendPlan kv4_attend_plan(int T, int max_new, int B, int q_heads, int heads, int D, int max_tokens, int window,
+                              int sinks);
+hipError_t launch_kv4_attend(const Kv4AttendPlan &p, const Kv4Cache &c, const Kv4Batch &s, const void *q, long long ldq,
+                             int q_heads, int dtype, float scale, int window, int sinks, void *out, void *ws,
+                             hipStream_t st);
+
+// ---- low-rank adapters ----
+// 16 mt rows a tile, tiles, parts of K, 256-column strips a workgroup takes in turn,
+// bytes of workspace.
+struct LoraPlan {
+    int mt, splits, strips;
+    long long tiles;
+    size_t bytes;
+};
+LoraPlan lora_plan(int T, int L, int K, int N, int R);
+hipError_t launch_lora(const LoraPlan &pl, const void *x, const void *a, const void *b, const float *scaling,
+                       const int32_t *off, const int32_t *rows, const int32_t *slots, int L, int T, int K, int N, int R,
+                       int dtype, void *y, void *ws, hipStream_t st);
+
 } // namespace qg
