@@ -3,20 +3,22 @@
 //
 // With K = kc ks + kz and V = vc vs + vz by token t and group g of channels,
 //   score[t]  = sum_g ks[t,g] (q_g . kc[t]_g) + kz[t,g] sum(q_g)
-//   out_g     = sum_t (p[t] vs[t,g]) vc[t]_g + sum_t p[t] vz[t,g]
-// so the codes go into the products as they are (exact binary16 subnormals, two ANDs
-// and a shift per four of them) and scales and zeros stay in 32 bits outside.  The
-// only operands rounded to 16 bits are p[t] vs[t,g]; the queries enter exactly, scaled
-// by a power of two of their row's largest value (bf16 ones too: eight bits of eleven).
+//   out_g     = sum_t (p[t] vs[t,g]) (vc[t]_g - 8) + sum_t p[t] (vz[t,g] + 8 vs[t,g])
+// so codes enter the products exactly: keys as the binary16 subnormals that an AND
+// leaves of their nibbles (two ANDs and half a shift for two of them), values, whose
+// partner p vs is rounded to 16 bits, around their middle, where that rounding costs a
+// third of what it would around 0 (a packed subtraction more).  The terms of the zeros
+// are one more product each, straight from the words in which scale and zero stand: for the
+// keys against sum(q_g) as two 16-bit values, for the values against p, together with
+// a row of ones that sums p up.  The queries enter exactly, scaled by a power of two of
+// their row's largest value (bf16 ones too: eight bits of eleven).
 //
 // A wave takes 16 NQ rows (the query heads of one key/value head, token by token) as
 // the columns of its products and the tokens as the rows: a lane then holds the scores of
 // one query row against four consecutive tokens of each of two 16-token tiles, which
-// is what the second product takes from it, and nothing goes through LDS.
+// is what the second product takes from it.
 #include "qg_kv4.h"
 #include "qg_launch.h"
-
-#include <type_traits>
 
 namespace qg {
 namespace {
@@ -39,39 +41,78 @@ constexpr float NONE = -3.0e38f;   // the running maximum before any token
 // binary16, and the rescaling of all accumulators is rare.
 constexpr float SLACK = 2.0f;
 
-// The two k-steps of a word pair (K), or the operand of one word (V).
+// A k-step of a pair of key words: their low (high) nibbles, 2^-24 (2^-20) each.
 __device__ inline half8 code_op(unsigned x, unsigned y, unsigned mask)
 {
     return __builtin_bit_cast(half8, uint4v{x & mask, x >> 8 & mask, y & mask, y >> 8 & mask});
 }
-__device__ inline half8 value_op(unsigned x)
+// The eight codes of a value word, less 8: a low nibble ORed into 0x6400 reads 1024 + v, a
+// high one into 0x5400 64 + v, and the subtraction is exact.
+__device__ inline half8 value_op(unsigned x, unsigned mag_lo, unsigned mag_hi)
 {
-    return __builtin_bit_cast(half8, uint4v{x & 0x000F000Fu, x >> 8 & 0x000F000Fu, x & 0x00F000F0u, x >> 8 & 0x00F000F0u});
+    const half2v off_lo = {(_Float16)1032.f, (_Float16)1032.f}, off_hi = {(_Float16)72.f, (_Float16)72.f};
+    const unsigned y = x >> 8;
+    auto lo = [&](unsigned v) {
+        return __builtin_bit_cast(unsigned, __builtin_bit_cast(half2v, and_or_b32(v, 0x000F000Fu, mag_lo)) - off_lo);
+    };
+    auto hi = [&](unsigned v) {
+        return __builtin_bit_cast(unsigned, __builtin_bit_cast(half2v, and_or_b32(v, 0x00F000F0u, mag_hi)) - off_hi);
+    };
+    return __builtin_bit_cast(half8, uint4v{lo(x), lo(y), hi(x), hi(y)});
+}
+
+// Whether either half of a word is no finite binary16.
+__device__ inline bool odd_word(unsigned w)
+{
+    return (w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u;
 }
 
 __device__ inline float lo16(unsigned x) { return h2f((uint16_t)x); }
-__device__ inline float hi16(unsigned x) { return h2f((uint16_t)(x >> 16)); }
 
+// 64 lanes' 16 bytes from global memory to LDS, lane after lane from `to` on (the same
+// for all lanes).
+template <int POLICY>
+__device__ inline void lds_load16(const uint32_t *from, uint8_t *to)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                     (__attribute__((address_space(3))) void *)to, 16, 0, POLICY);
+}
+
+template <int N>
+__device__ inline void wait_loads()
+{
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// A wave's ring of 32-token blocks in LDS.  Loads go there directly: keys and values
+// as they lie, then scales and zeros, [keys | values][group][32] words (repeated up
+// to whole loads of 64 lanes).
 template <int D, int NG>
-struct Stage {
-    static constexpr int NW = D / 32;
-    unsigned k[2][NW];
-    uint4v v[D / 64];
-    uint4v ks[NG][2], vs[NG][2];
-    int t0;
-    bool ok;
+struct Ring {
+    static constexpr int STAGES = 2;
+    static constexpr int CODES = 32 * D / 2;                       // bytes of a block's keys, or of its values
+    static constexpr int SCALES = NG > 4 ? 256 * NG : 1024;
+    static constexpr int BYTES = 2 * CODES + SCALES;
+    static constexpr int LOADS = BYTES / 1024;
 };
 
 // MERGE: the workgroup's four waves share 16 NQ rows and take every fourth block of
 // tokens; their results meet in LDS at the end.  Otherwise each wave has rows of its own.
 template <int D, int NG, int NQ, bool MERGE>
-__global__ __launch_bounds__(256) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s, AttendArgs a)
+__global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s, AttendArgs a)
 {
     constexpr int NW = D / 32, DT = D / 16, SPG = NW / NG, TPG = DT / NG;
     constexpr int ROWS = 16 * NQ, RB = MERGE ? ROWS : 4 * ROWS;
+    using RG = Ring<D, NG>;
+    constexpr int LD = D + 4;                              // (a row of the waves' results)
+    constexpr int RINGS = 4 * RG::STAGES * RG::BYTES, SUMS = MERGE ? 4 * 16 * (LD + 2) * 4 : 0;
+    // (one array for all: with several the compiler puts a wait for all loads before each
+    // read of the ring)
+    __shared__ __attribute__((aligned(16))) uint8_t lds[RINGS > SUMS ? RINGS : SUMS];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, kq = lane >> 4;
     const int H = c.heads, R = a.R;
+    uint8_t *const ring = lds + w * (RG::STAGES * RG::BYTES);
     const int h = blockIdx.x % H, xs = blockIdx.x / H;
     const int split = xs % a.splits;
     int b, in, of;
@@ -104,9 +145,8 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s,
     const int j0 = split * per, j1 = j0 + per < nb ? j0 + per : nb;
     const int step = MERGE ? 4 : 1;
 
-    // the rows: operand, group sums, factor of their scores, position
-    half8 qo[NQ][NW];
-    float qs[NQ][NG], f[NQ];
+    // the rows' queries, and positions
+    uint4v raw[NQ][NW];
     int pos[NQ];
     size_t grow[NQ];                                       // row of [T * q_heads]
 #pragma unroll
@@ -118,27 +158,75 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s,
         grow[n] = t * a.q_heads + (size_t)h * R + hr;
         pos[n] = live ? first + i : -1;
         const uint16_t *const p = a.q + t * a.ldq + ((size_t)h * R + hr) * D + 8 * kq;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) raw[n][k] = *reinterpret_cast<const uint4v *>(p + 32 * k);
+    }
+
+    // a wave's blocks: every `step`-th from j0 + (its number) on
+    const int mine = j1 <= j0 ? 0 : (MERGE ? (j1 - j0 - w + 3) / 4 : j1 - j0);
+    auto block_of = [&](int i) {
+        const int j = j0 + (MERGE ? w : 0) + i * step;
+        return j < ns ? j : j - ns + w0;
+    };
+    auto page_of = [&](int i) { return s.table[(size_t)b * s.width + (block_of(i) >> (c.shift - 5))]; };
+    constexpr int SLOADS = RG::SCALES / 1024;
+    const uint32_t *sz0[SLOADS];
+#pragma unroll
+    for (int u = 0; u < SLOADS; ++u) {
+        const int piece = (8 * u + lane / 8) % (2 * NG);
+        sz0[u] = (piece < NG ? c.k_sz : c.v_sz) + ((size_t)(piece % NG) << c.shift) + lane % 8 * 4;
+    }
+    auto load = [&](int i, int pg) {
+        const int t0 = block_of(i) << 5, tin = t0 & ((1 << c.shift) - 1);
+        const size_t head = (size_t)((unsigned)pg < (unsigned)c.pages ? pg : 0) * H + h;
+        const size_t at = ((head << c.shift) + tin) * (D / 8);
+        uint8_t *const to = ring + (i % RG::STAGES) * RG::BYTES;
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) lds_load16<0>(c.k + at + u * 256 + lane * 4, to + u * 1024);
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) lds_load16<0>(c.v + at + u * 256 + lane * 4, to + RG::CODES + u * 1024);
+        const size_t sat = ((head * NG) << c.shift) + tin;
+#pragma unroll
+        for (int u = 0; u < SLOADS; ++u) lds_load16<0>(sz0[u] + sat, to + 2 * RG::CODES + u * 1024);
+    };
+
+    // pages are asked for two blocks ahead, blocks one
+    int pg = 0, next = 0;
+    if (mine > 0) {
+        pg = page_of(0);
+        next = page_of(mine > 1 ? 1 : 0);
+        load(0, pg);
+    }
+
+    // the queries as operands, q' = q 2^(15 - ex) below 2^15 (sixteenths against the high
+    // nibbles); the factor of the scores (the codes weigh 2^-24); the groups' sums as two
+    // 16-bit values, against the zeros in the words of lane groups 0 (the upper part) and 1
+    half8 qo[NQ][NW], qz[NQ];
+    float f[NQ];
+    constexpr int GL = NG > 4 ? 2 : 1;                     // lane groups that the groups' words take
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
         float x[NW][8], big = 0.0f;
         bool bad = false;
+        const bool live = pos[n] >= 0 || row0 + 16 * n + col < rows;
 #pragma unroll
-        for (int k = 0; k < NW; ++k) {
-            const uint4v raw = *reinterpret_cast<const uint4v *>(p + 32 * k);
+        for (int k = 0; k < NW; ++k)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint16_t v = (uint16_t)(raw[e >> 1] >> (16 * (e & 1)));
-                x[k][e] = live ? (a.bf16 ? bf2f(v) : h2f(v)) : 0.0f;
+                const uint16_t v = live ? (uint16_t)(raw[n][k][e >> 1] >> (16 * (e & 1))) : 0;
+                const float fb = bf2f(v), fh = h2f(v);
+                x[k][e] = a.bf16 ? fb : fh;
                 bad |= !(__builtin_fabsf(x[k][e]) < __builtin_inff());
                 big = fmaxf(big, __builtin_fabsf(x[k][e]));
             }
-        }
         big = fmaxf(big, __shfl_xor(big, 16));
         big = fmaxf(big, __shfl_xor(big, 32));
         bad |= __shfl_xor((int)bad, 16) != 0;
         bad |= __shfl_xor((int)bad, 32) != 0;
         int ex = 0;
         if (big > 0.0f && !bad) (void)frexpf(big, &ex);    // big < 2^ex
-        // q' = q 2^(15 - ex), below 2^15; the codes weigh 2^-24
         f[n] = bad ? __builtin_nanf("") : ldexpf(a.scale, ex + 9);
+        float qs[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             float sum = 0.0f;
@@ -152,97 +240,102 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s,
                 }
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
-            qs[n][g] = sum * 0x1p-24f;
+            qs[g] = sum * 0x1p-24f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float v = 0.0f;
+            if (NG > 4)
+                v = (kq & 1) ? qs[(4 + i) % NG] : qs[i % NG];
+            else if (i < NG)
+                v = qs[i];
+            const _Float16 hi = (_Float16)v;
+            const _Float16 part = kq / GL == 0 ? hi : kq / GL == 1 ? (_Float16)(v - (float)hi) : (_Float16)0.0f;
+            qz[n][2 * i] = (_Float16)0.0f;
+            qz[n][2 * i + 1] = part;
         }
     }
 
-    float m[NQ], l[NQ][2], z[NQ][NG][2];
-    float4v o[NQ][DT];
+    // running maximum; products with the values' codes; with their scales (even rows) and
+    // zeros (odd), and with ones (row 2 NG: the sum of p; with eight groups no row is left)
+    constexpr bool LROW = 2 * NG < 16;
+    float m[NQ], l[NQ];
+    float4v o[NQ][DT], z[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
         m[n] = NONE;
-        l[n][0] = l[n][1] = 0.0f;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) z[n][g][0] = z[n][g][1] = 0.0f;
+        l[n] = 0.0f;
+        z[n] = float4v{0, 0, 0, 0};
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[n][d] = float4v{0, 0, 0, 0};
     }
+    unsigned mag_lo = 0x64006400u, mag_hi = 0x54005400u;
+    pin(mag_lo);
+    pin(mag_hi);
 
-    auto load = [&](Stage<D, NG> &x, int j) {
-        const int blk = j < ns ? j : j - ns + w0;
-        x.t0 = blk << 5;
-        const int pg = s.table[(size_t)b * s.width + (x.t0 >> c.shift)];
-        x.ok = (unsigned)pg < (unsigned)c.pages;
-        const size_t head = (size_t)(x.ok ? pg : 0) * H + h;
-        const int tin = x.t0 & ((1 << c.shift) - 1);
-        const size_t at = ((head << c.shift) + tin) * (D / 8);
-        const uint32_t *const kp = c.k + at + col * (D / 8) + kq * NW;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            if constexpr (NW == 2) {
-                const uint2v r = *reinterpret_cast<const uint2v *>(kp + t * 16 * (D / 8));
-                x.k[t][0] = r.x;
-                x.k[t][1] = r.y;
-            } else {
-#pragma unroll
-                for (int i = 0; i < NW / 4; ++i) {
-                    const uint4v r = *reinterpret_cast<const uint4v *>(kp + t * 16 * (D / 8) + 4 * i);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x.k[t][4 * i + e] = r[e];
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < D / 64; ++u)
-            x.v[u] = *reinterpret_cast<const uint4v *>(c.v + at + u * 256 + lane * 4);
-        const size_t sat = ((head * NG) << c.shift) + tin + 4 * kq;
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                x.ks[g][t] = *reinterpret_cast<const uint4v *>(c.k_sz + sat + ((size_t)g << c.shift) + 16 * t);
-                x.vs[g][t] = *reinterpret_cast<const uint4v *>(c.v_sz + sat + ((size_t)g << c.shift) + 16 * t);
-            }
-    };
-
-    auto compute = [&](const Stage<D, NG> &x, auto masked) {
-        constexpr bool MASK = decltype(masked)::value;
+    auto block = [&](const uint8_t *x, int t0, bool ok) {
+        const uint4v *const ksz = reinterpret_cast<const uint4v *>(x + 2 * RG::CODES) + kq;
+        const uint4v *const vsz = ksz + NG * 8;
+        const unsigned *const kw = reinterpret_cast<const unsigned *>(x + 2 * RG::CODES) + col;
         float4v sc[NQ][2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             half8 op[NW];
+            const uint8_t *const kt = x + t * (RG::CODES / 2) + (col * 4 + kq) * (D / 8);
 #pragma unroll
-            for (int i = 0; i < NW / 2; ++i) {
-                op[i] = code_op(x.k[t][2 * i], x.k[t][2 * i + 1], 0x000F000Fu);
-                op[i + NW / 2] = code_op(x.k[t][2 * i], x.k[t][2 * i + 1], 0x00F000F0u);
+            for (int i = 0; i < NW / 2; i += 2) {
+                uint4v r = {0, 0, 0, 0};
+                if constexpr (NW == 2) {
+                    const uint2v r2 = *reinterpret_cast<const uint2v *>(kt);
+                    r.x = r2.x;
+                    r.y = r2.y;
+                } else {
+                    r = *reinterpret_cast<const uint4v *>(kt + 8 * i);
+                }
+                op[i] = code_op(r.x, r.y, 0x000F000Fu);
+                op[i + NW / 2] = code_op(r.x, r.y, 0x00F000F0u);
+                if constexpr (NW > 2) {
+                    op[i + 1] = code_op(r.z, r.w, 0x000F000Fu);
+                    op[i + 1 + NW / 2] = code_op(r.z, r.w, 0x00F000F0u);
+                }
             }
+            uint4v zw = {0, 0, 0, 0};                      // this lane's token: (scale, zero) of four groups
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
+            for (int i = 0; i < (NG < 4 ? NG : 4); ++i)
+                zw[i] = kw[(NG > 4 ? (kq & 1) * 4 + i : i) * 32 + 16 * t];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+                sc[n][t] = mfma_f16(__builtin_bit_cast(half8, zw), qz[n], float4v{0, 0, 0, 0});
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const uint4v sz = ksz[g * 8 + t * 4];
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
                     float4v acc = {0, 0, 0, 0};
 #pragma unroll
                     for (int k = g * SPG; k < (g + 1) * SPG; ++k) acc = mfma_f16(op[k], qo[n][k], acc);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float zero = hi16(x.ks[g][t][r]) * qs[n][g];
-                        sc[n][t][r] = lo16(x.ks[g][t][r]) * acc[r] + (g ? sc[n][t][r] + zero : zero);
-                    }
+                    for (int r = 0; r < 4; ++r) sc[n][t][r] = __builtin_fmaf(lo16(sz[r]), acc[r], sc[n][t][r]);
                 }
+            }
         }
-        bool vis[NQ][2][4];
-        if (MASK) {
+        // all rows see all of the block, or some do not: a bit for each score that is hidden
+        const bool whole = ok && t0 + 31 <= p0 && (!a.window || t0 > p1 - a.window || t0 + 31 < a.sinks);
+        unsigned hide[NQ];
+        if (!whole) {
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
+            for (int n = 0; n < NQ; ++n) {
+                hide[n] = 0;
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const int at = x.t0 + 16 * t + 4 * kq + r;
-                        vis[n][t][r] = x.ok && at <= pos[n] &&
-                                       (!a.window || at > pos[n] - a.window || at < a.sinks);
-                        if (!vis[n][t][r]) sc[n][t][r] = -__builtin_inff();
+                        const int at = t0 + 16 * t + 4 * kq + r;
+                        const bool vis = ok && at <= pos[n] && (!a.window || at > pos[n] - a.window || at < a.sinks);
+                        hide[n] |= vis ? 0u : 1u << (4 * t + r);
+                        sc[n][t][r] = vis ? sc[n][t][r] : -__builtin_inff();
                     }
+            }
         }
         bool raise = false;
         float mx[NQ];
@@ -260,15 +353,28 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s,
                 v = fmaxf(m[n], fmaxf(v, __shfl_xor(v, 32)));
                 const float by = __builtin_amdgcn_exp2f(m[n] - v);
                 m[n] = v;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    l[n][t] *= by;
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) z[n][g][t] *= by;
-                }
+                l[n] *= by;
+                z[n] *= by;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[n][d] *= by;
             }
+        }
+        half8 pf[NQ];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    sc[n][t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][t][r], f[n], -m[n]));
+        if (!whole) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (hide[n] >> (4 * t + r) & 1) sc[n][t][r] = 0.0f;
         }
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
@@ -276,77 +382,114 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s,
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    // the second tile's codes are the high nibbles: 16 times as large
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][t][r], f[n], -(m[n] + (t ? 4.0f : 0.0f))));
-                    sc[n][t][r] = MASK && !vis[n][t][r] ? 0.0f : p;
-                    l[n][t] += sc[n][t][r];
+                    pf[n][4 * t + r] = (_Float16)sc[n][t][r];
+                    if (!LROW) l[n] += sc[n][t][r];
                 }
-        half8 vo[DT];
+
+        // the rows of scales and zeros: lane (col, kq) takes the halves of one kind of group
+        // col / 2, of the eight tokens of lane group kq
+        const int zg = col / 2 < NG ? col / 2 : 0;
+        uint4v za[2], zh;
 #pragma unroll
-        for (int d = 0; d < DT; ++d) vo[d] = value_op(x.v[d / 4][d % 4]);
+        for (int t = 0; t < 2; ++t) za[t] = vsz[zg * 8 + t * 4];
+        if (!whole) {
+            // a token that one row sees and another does not must not bring it a NaN: 0 here, and a NaN
+            // put in where it is seen
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                half8 po;
+                for (int r = 0; r < 4; ++r) za[t][r] = odd_word(za[t][r]) ? 0u : za[t][r];
+        }
+        const unsigned sel = (col & 1) ? 0x07060302u : 0x05040100u;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            zh[2 * t] = __builtin_amdgcn_perm(za[t][1], za[t][0], sel);
+            zh[2 * t + 1] = __builtin_amdgcn_perm(za[t][3], za[t][2], sel);
+        }
+        if (LROW && col >= 2 * NG) zh = uint4v{0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) z[n] = mfma_f16(__builtin_bit_cast(half8, zh), pf[n], z[n]);
+
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            uint4v sz[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) sz[t] = vsz[g * 8 + t * 4];
+            if (!whole) {
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    bool nan = false;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) nan |= odd_word(sz[t][r]) && !(hide[n] >> (4 * t + r) & 1);
+                    if (__any(nan)) {
+                        int any = nan;
+                        any |= __shfl_xor(any, 16);
+                        any |= __shfl_xor(any, 32);
+                        if (any && kq == g / 2) z[n][2 * (g % 2)] = __builtin_nanf("");
+                    }
+                }
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float vs = lo16(x.vs[g][t][r]), vz = hi16(x.vs[g][t][r]);
-                        if (MASK) {
-                            vs = vis[n][t][r] ? vs : 0.0f;
-                            vz = vis[n][t][r] ? vz : 0.0f;
-                        }
-                        po[4 * t + r] = (_Float16)(sc[n][t][r] * vs);
-                        z[n][g][t] = __builtin_fmaf(sc[n][t][r], vz, z[n][g][t]);
-                    }
-#pragma unroll
-                for (int d = g * TPG; d < (g + 1) * TPG; ++d) o[n][d] = mfma_f16(vo[d], po, o[n][d]);
+                    for (int r = 0; r < 4; ++r) sz[t][r] = odd_word(sz[t][r]) ? 0u : sz[t][r];
             }
+            half8 po[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) po[n][4 * t + r] = (_Float16)__builtin_fmaf(lo16(sz[t][r]), sc[n][t][r], 0.0f);
+#pragma unroll
+            for (int d = g * TPG; d < (g + 1) * TPG; ++d) {
+                const half8 vo = value_op(*reinterpret_cast<const unsigned *>(x + RG::CODES + d / 4 * 1024 + lane * 16 + d % 4 * 4),
+                                          mag_lo, mag_hi);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) o[n][d] = mfma_f16(vo, po[n], o[n][d]);
+            }
+        }
     };
 
-    auto block = [&](const Stage<D, NG> &x) {
-        debug_stage_sync();
-        // all rows see all of the block, or some do not
-        const bool whole = x.ok && x.t0 + 31 <= p0 &&
-                           (!a.window || x.t0 > p1 - a.window || x.t0 + 31 < a.sinks);
-        if (whole)
-            compute(x, std::false_type{});
-        else
-            compute(x, std::true_type{});
-    };
-
-    for (int j = j0 + (MERGE ? w : 0); j < j1; j += step) {
-        Stage<D, NG> x;
-        load(x, j);
-        block(x);
+    for (int i = 0; i < mine; ++i) {
+        const int here = pg;
+        pg = next;
+        if (i + 1 < mine) {
+            next = page_of(i + 2 < mine ? i + 2 : i + 1);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage's last reads are done
+            load(i + 1, pg);
+            debug_stage_sync();
+            wait_loads<RG::LOADS>();
+        } else {
+            wait_loads<0>();
+        }
+        block(ring + (i % RG::STAGES) * RG::BYTES, block_of(i) << 5, (unsigned)here < (unsigned)c.pages);
     }
 
-    // a column's sums over its four lanes, and its values with the zeros' part
+    // a column's sum of p, and its values with the zeros' part, from the lane groups that hold them
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-        float sum = l[n][0] + 16.0f * l[n][1];
-        sum += __shfl_xor(sum, 16);
-        sum += __shfl_xor(sum, 32);
-        l[n][0] = sum;
+        if (LROW) {
+            l[n] = __shfl(z[n][2 * NG % 4], 16 * (2 * NG / 4 % 4) + col);
+        } else {
+            l[n] += __shfl_xor(l[n], 16);
+            l[n] += __shfl_xor(l[n], 32);
+        }
+        const float zz[2] = {__builtin_fmaf(z[n][0], 8.0f, z[n][1]), __builtin_fmaf(z[n][2], 8.0f, z[n][3])};
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            float zs = z[n][g][0] + 16.0f * z[n][g][1];
-            zs += __shfl_xor(zs, 16);
-            zs += __shfl_xor(zs, 32);
+            const float zs = __shfl(zz[g % 2], 16 * (g / 2) + col);
 #pragma unroll
-            for (int d = g * TPG; d < (g + 1) * TPG; ++d)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) o[n][d][r] = __builtin_fmaf(o[n][d][r], 0x1p24f, zs);
+            for (int d = g * TPG; d < (g + 1) * TPG; ++d) o[n][d] += zs;
         }
     }
 
     const size_t all = (size_t)s.T * a.q_heads;
     if constexpr (MERGE) {
-        constexpr int LD = D + 4;
-        __shared__ float so[4][16][LD];
-        __shared__ float sm[4][16], sl[4][16];
+        float(*const so)[16][LD] = reinterpret_cast<float(*)[16][LD]>(lds);
+        float(*const sm)[16] = reinterpret_cast<float(*)[16]>(lds + 4 * 16 * LD * 4), (*const sl)[16] = sm + 4;
+        __syncthreads();                                   // (the waves' rings are done with)
         // what a thread adds up: four channels of a row
         constexpr int TPR = D / 4, PASS = 256 / TPR;
 #pragma unroll
@@ -357,7 +500,7 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s,
                 *reinterpret_cast<float4v *>(&so[w][col][16 * d + 4 * kq]) = o[n][d];
             if (kq == 0) {
                 sm[w][col] = m[n];
-                sl[w][col] = l[n][0];
+                sl[w][col] = l[n];
             }
             debug_stage_sync();
             __syncthreads();
@@ -399,7 +542,7 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s,
             if (a.splits > 1) {
                 if (kq == 0) {
                     a.ml[(split * all + grow[n]) * 2] = m[n];
-                    a.ml[(split * all + grow[n]) * 2 + 1] = l[n][0];
+                    a.ml[(split * all + grow[n]) * 2 + 1] = l[n];
                 }
                 if (j0 < j1)
 #pragma unroll
@@ -407,7 +550,7 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s,
                         *reinterpret_cast<float4v *>(a.part + (split * all + grow[n]) * D + 16 * d + 4 * kq) = o[n][d];
                 continue;
             }
-            const float inv = l[n][0] == 0.0f ? 0.0f : 1.0f / l[n][0];
+            const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
                 uint16_t v[4];
@@ -420,8 +563,10 @@ __global__ __launch_bounds__(256) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s,
     }
 }
 
-// The parts of a row, one workgroup a row: groups of D / 4 threads take every further
-// part, then meet in LDS.  Parts without a token hold sum 0 and no values.
+// The parts of a row, one workgroup a row: a thread takes a part's maximum and sum, then
+// groups of D / 4 threads every further part's values, and they meet in LDS.  Parts
+// without a token hold sum 0 and no values.
+constexpr int MAX_SPLITS = 128;
 template <int D>
 __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Batch s, AttendArgs a)
 {
@@ -431,30 +576,46 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Batch s, AttendArgs a)
         const long long t = (long long)(g / a.q_heads);
         if (t < s.off[0] || t >= s.off[s.B]) return;
     }
-    const int grp = threadIdx.x / TPR, ch = threadIdx.x % TPR * 4;
-    float m = NONE;
-    for (int i = 0; i < a.splits; ++i) m = fmaxf(m, a.ml[(i * all + g) * 2]);
-    float sum = 0.0f;
-    float4v acc = {0, 0, 0, 0};
-    for (int i = grp; i < a.splits; i += GR) {
-        const float mi = a.ml[(i * all + g) * 2], li = a.ml[(i * all + g) * 2 + 1];
-        if (li == 0.0f) continue;
-        const float by = __builtin_amdgcn_exp2f(mi - m);
-        sum += by * li;
-        acc += by * *reinterpret_cast<const float4v *>(a.part + (i * all + g) * D + ch);
-    }
+    const int tid = threadIdx.x, grp = tid / TPR, ch = tid % TPR * 4;
     __shared__ float4v so[GR][TPR];
-    __shared__ float sl[GR];
-    so[grp][threadIdx.x % TPR] = acc;
-    if (ch == 0) sl[grp] = sum;
+    __shared__ float by[MAX_SPLITS], top[2], total[2];
+    // (two waves hold the parts)
+    float mi = NONE, li = 0.0f;
+    if (tid < a.splits) {
+        mi = a.ml[(tid * all + g) * 2];
+        li = a.ml[(tid * all + g) * 2 + 1];
+    }
+    float m = mi;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+    if (tid < MAX_SPLITS && tid % 64 == 0) top[tid / 64] = m;
+    debug_stage_sync();
+    __syncthreads();
+    m = fmaxf(top[0], top[1]);
+    if (tid < MAX_SPLITS) {
+        const float e = __builtin_amdgcn_exp2f(mi - m);
+        // a part without a token has no values to be read
+        by[tid] = li == 0.0f ? 0.0f : e;
+        li = li == 0.0f ? 0.0f : li * e;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) li += __shfl_xor(li, o);
+        if (tid % 64 == 0) total[tid / 64] = li;
+    }
+    debug_stage_sync();
+    __syncthreads();
+    float4v acc = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int i = grp; i < a.splits; i += GR) {
+        const float e = by[i];
+        if (e != 0.0f) acc += e * *reinterpret_cast<const float4v *>(a.part + (i * all + g) * D + ch);
+    }
+    so[grp][tid % TPR] = acc;
     debug_stage_sync();
     __syncthreads();
     if (grp) return;
 #pragma unroll
-    for (int i = 1; i < GR; ++i) {
-        acc += so[i][threadIdx.x];
-        sum += sl[i];
-    }
+    for (int i = 1; i < GR; ++i) acc += so[i][tid];
+    const float sum = total[0] + total[1];
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     uint16_t v[4];
 #pragma unroll
@@ -484,17 +645,23 @@ Kv4AttendPlan kv4_attend_plan(int T, int max_new, int B, int q_heads, int heads,
     p.shared = max_new * R <= 16;
     p.rows = p.shared || D == 256 ? 16 : 32;
     const int rb = p.shared ? p.rows : 4 * p.rows;
-    // row blocks of all sequences: each has at most one that is not full
-    const long long blocks = T * R / rb + (T < B ? T : B);
+    // row blocks of all sequences: each has at most one that is not full.  (The grid holds
+    // them whatever max_new says; where it says that a sequence has one at most, parts are
+    // made for that many.)
+    const long long some = T < B ? T : B;
+    const long long blocks = T * R / rb + some;
+    const long long likely = (max_new * R <= rb ? some : blocks) * heads;
     long long tokens = max_tokens;
     if (window > 0) {
         const long long seen = (long long)window + sinks + max_new + 64;
         tokens = seen < tokens ? seen : tokens;
     }
-    const long long most = (tokens + 127) / 128;          // four blocks of tokens to a part
-    long long n = (1024 + blocks * heads - 1) / (blocks * heads);
+    // parts along the tokens fill the CUs once (three workgroups each of 64 or 128 shared
+    // channels, else two), of at least a block of tokens for each wave
+    const long long most = (tokens + 127) / 128, fit = p.shared && D < 256 ? 768 : 512;
+    long long n = fit / likely;
     n = n > most ? most : n;
-    n = n > 128 ? 128 : n;
+    n = n > MAX_SPLITS ? MAX_SPLITS : n;
     p.splits = n < 1 ? 1 : (int)n;
     p.workgroups = blocks * heads * p.splits;
     p.bytes = p.splits == 1 ? 0 : (size_t)p.splits * T * q_heads * (D + 2) * sizeof(float);

@@ -101,17 +101,23 @@ def attend(q, cache, lens, off, table, scale, window=0, sinks=0):
 
     The tolerance adds up, for each value:
       * its rounding to q's type: half a step, eps / 2 of it;
-      * p_t * s_t rounded to fp16 (2^-11 of it, 2^-25 where it is subnormal, and that 16
-        times as much in the tile whose codes are held 16-fold), times the code;
+      * with V = s c + z written as s (c - 8) + m, m = z + 8 s: p_t s_t rounded to fp16 (2^-11 of it,
+        2^-25 where it is subnormal) against c - 8, and p_t rounded to fp16 against m and in
+        its sum (the same again, of the sum of p |m| and of the value);
       * p_t in 32 bits: the score's sum of D products (2^-24 of their sizes for each of
         the D/32 + 8 additions in a row), its product with the scale, and 2^-22 for
-        the exponential; the same for their sum.
+        the exponential; the same for their sum;
+      * the sum of a group's queries as two 16-bit values, 2^-25 of 2^-9 of a power of two
+        over the row's largest query and up to twice that: 2^-16 times 2 max |q| times |z|;
+      * products and sums in 32 bits, 2^-20 of their sizes.
     """
     kd, vd = values_of(cache)
     vc = codes_of(cache)[1].double()
     page, H, D, g = cache.page_size, cache.heads, cache.head_dim, cache.group
     vs = cache.v_sz[..., 0].cpu().double().transpose(2, 3).repeat_interleave(g, -1)
-    codep = vc * vs
+    vz = cache.v_sz[..., 1].cpu().double().transpose(2, 3).repeat_interleave(g, -1)
+    kz = cache.k_sz[..., 1].cpu().double().abs().amax(2)[..., None]      # [pages, heads, page, 1]: a token's largest
+    codep, mid = (vc - 8).abs() * vs, (vz + 8 * vs).abs()
     R = q.shape[1] // H
     out = torch.zeros(q.shape, dtype=torch.float64)
     tol = torch.zeros(q.shape, dtype=torch.float64)
@@ -123,6 +129,8 @@ def attend(q, cache, lens, off, table, scale, window=0, sinks=0):
         k, has = rows_of(kd, table, b, n, page)
         v, _ = rows_of(vd, table, b, n, page)
         c, _ = rows_of(codep, table, b, n, page)
+        mm, _ = rows_of(mid, table, b, n, page)
+        zz, _ = rows_of(kz, table, b, n, page)
         t = torch.arange(n)
         for i in range(r0, r1):
             pos = n - (r1 - r0) + (i - r0)
@@ -132,7 +140,7 @@ def attend(q, cache, lens, off, table, scale, window=0, sinks=0):
             if not bool(seen.any()):
                 continue
             for h in range(H):
-                kk, vv, cc = k[seen, h], v[seen, h], c[seen, h]
+                kk, vv, cc, md = k[seen, h], v[seen, h], c[seen, h], mm[seen, h]
                 for r in range(R):
                     qq = q[i, h * R + r].double()
                     x = kk @ qq * scale
@@ -141,8 +149,9 @@ def attend(q, cache, lens, off, table, scale, window=0, sinks=0):
                     out[i, h * R + r] = o
                     size = kk.abs() @ qq.abs() * scale
                     e = size.max() * (D / 32 + 8) * 2.0**-24 + x.abs().max() * 2.0**-23 + 2.0**-22
-                    flat = 240 * 2.0**-25 * len(x) / torch.exp(x - x.max()).sum()
-                    tol[i, h * R + r] = (half * o.abs() + 2.0**-11 * (p @ cc.abs()) + flat +
+                    e = e + zz[seen, h].max() * 2 * qq.abs().max() * 2.0**-16 * (D // g) * scale
+                    flat = 2.0**-25 * len(x) / torch.exp(x - x.max()).sum() * (8 + md.amax(0) + o.abs())
+                    tol[i, h * R + r] = (half * o.abs() + 2.0**-11 * (p @ cc + p @ md + o.abs()) + flat +
                                          2 * e * (p @ vv.abs() + o.abs()) + 2.0**-20 * (p @ vv.abs()))
     return out, tol * 1.01 + 1e-30
 
