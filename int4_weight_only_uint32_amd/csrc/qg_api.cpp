@@ -947,7 +947,9 @@ int lora_add(const void *X, const void *A, const void *B, const float *scaling, 
         !aligned(adapter_offsets, 4) || !aligned(row_token, 4) || !aligned(slot_row, 4))
         return fail(QG_ERR_INVALID_ARG, "%s: misaligned pointer", what);
     const qg::LoraPlan plan = qg::lora_plan(T, L, K, N, R);
-    if (plan.tiles * 256 > MAX_GRID_THREADS) return fail(QG_ERR_UNSUPPORTED, "%s: T=%d too large for one launch", what, T);
+    if (plan.tiles * plan.ranges * 256 > MAX_GRID_THREADS || plan.narrow * 256 > MAX_GRID_THREADS ||
+        (long long)T * ((R + 63) / 64) * 8 > MAX_GRID_THREADS - 256)
+        return fail(QG_ERR_UNSUPPORTED, "%s: T=%d too large for one launch", what, T);
     if (!workspace || workspace_bytes < plan.bytes)
         return fail(QG_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, got %zu", what, plan.bytes,
                     workspace ? workspace_bytes : (size_t)0);
@@ -957,8 +959,8 @@ int lora_add(const void *X, const void *A, const void *B, const float *scaling, 
                                        Y, workspace, (hipStream_t)stream),
                        what, (hipStream_t)stream);
     if (rc == QG_OK)
-        log_first("%s T=%d L=%d K=%d N=%d R=%d %s: %d-row tiles, K in %d parts", what, T, L, K, N, R,
-                  dtype == QG_DTYPE_BF16 ? "bf16" : "fp16", 16 * plan.mt, plan.splits);
+        log_first("%s T=%d L=%d K=%d N=%d R=%d %s: narrow product in %d-row tiles and %d parts of K, wide one in %d-row tiles", what, T,
+                  L, K, N, R, dtype == QG_DTYPE_BF16 ? "bf16" : "fp16", plan.narrow_rows, plan.splits, plan.tall ? 128 : 16);
     return rc;
 }
 

@@ -248,6 +248,15 @@ constexpr unsigned waitcnt_vm(int n)
     return (unsigned)((n & 0xF) | ((n >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
 
+// 64 lanes' 16 bytes from global memory to LDS, lane after lane from `to` on (the same
+// for all lanes).
+template <int POLICY>
+__device__ inline void lds_load16(const uint32_t *from, uint8_t *to)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                     (__attribute__((address_space(3))) void *)to, 16, 0, POLICY);
+}
+
 __device__ inline float4v mfma_f16(half8 a, half8 b, float4v c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);

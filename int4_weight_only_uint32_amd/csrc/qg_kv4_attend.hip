@@ -69,15 +69,6 @@ __device__ inline bool odd_word(unsigned w)
 
 __device__ inline float lo16(unsigned x) { return h2f((uint16_t)x); }
 
-// 64 lanes' 16 bytes from global memory to LDS, lane after lane from `to` on (the same
-// for all lanes).
-template <int POLICY>
-__device__ inline void lds_load16(const uint32_t *from, uint8_t *to)
-{
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                     (__attribute__((address_space(3))) void *)to, 16, 0, POLICY);
-}
-
 template <int N>
 __device__ inline void wait_loads()
 {

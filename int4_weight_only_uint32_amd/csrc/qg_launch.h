@@ -195,11 +195,13 @@ hipError_t launch_kv4_attend(const Kv4AttendPlan &p, const Kv4Cache &c, const Kv
                              hipStream_t st);
 
 // ---- low-rank adapters ----
-// 16 mt rows a tile, tiles, parts of K, 256-column strips a workgroup takes in turn,
-// bytes of workspace.
+// Narrow product: rows a tile, parts of K, tiles.  Wide one: whether its tiles are 128 rows, tiles, column
+// ranges, strips of columns a workgroup takes in turn.  Bytes of workspace.
 struct LoraPlan {
-    int mt, splits, strips;
-    long long tiles;
+    int narrow_rows, splits;
+    bool tall;
+    int strips, ranges;
+    long long narrow, tiles;
     size_t bytes;
 };
 LoraPlan lora_plan(int T, int L, int K, int N, int R);

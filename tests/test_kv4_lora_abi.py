@@ -129,7 +129,7 @@ def test_lora_refusals(kw, rc):
 def test_lora_workspace_sizes():
     f = qg.qg_workspace_bytes
     assert f(qg.QG_OP_LORA, 0, 128, 256, 16, 3) == 0
-    assert f(qg.QG_OP_LORA, 4, 128, 256, 16, 3) % (4 * 16 * 4) == 0
+    assert f(qg.QG_OP_LORA, 4, 128, 256, 16, 3) >= 4 * 16 * 4      # sums of 16 columns for four rows
     for args in ((-1, 128, 256, 16, 3), (4, 12, 256, 16, 3), (4, 128, 256, 12, 3), (4, 128, 256, 16, 0)):
         with pytest.raises(qg.QGemmError):
             f(qg.QG_OP_LORA, *args)
