@@ -518,9 +518,10 @@ int kv4_read(const uint32_t *cache_k, const uint32_t *cache_v, const uint16_t *c
  * max_new  the expected largest number of rows of a sequence: it only picks the
  *          kernel, so a wrong one is slower, never wrong.
  * Scores, the softmax's maximum and sum and the accumulators are fp32; the
- * queries and codes enter the products exactly (a query's channels down to
- * 2^-24 of its largest), p_t * s_t rounded to fp16 once.  Results depend on the
- * arguments' sizes, not on timing.
+ * codes enter the products exactly, and so do a query's channels down to
+ * 2^-17 of its largest (smaller ones within 2^-28 of that); p_t, against zeros
+ * and in the sum, and p_t * s_t, against codes, are rounded to fp16 once each.
+ * Results depend on the arguments alone, not on timing.
  * workspace  kv4_attend_workspace_bytes(...) bytes, 256-byte aligned (NULL when
  *          0); nothing is kept in it between calls.  One or two kernels.     */
 size_t kv4_attend_workspace_bytes(int T, int max_new, int B, int q_heads, int heads, int head_dim,

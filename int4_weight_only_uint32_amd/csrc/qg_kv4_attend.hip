@@ -4,14 +4,14 @@
 // With K = kc ks + kz and V = vc vs + vz by token t and group g of channels,
 //   score[t]  = sum_g ks[t,g] (q_g . kc[t]_g) + kz[t,g] sum(q_g)
 //   out_g     = sum_t (p[t] vs[t,g]) (vc[t]_g - 8) + sum_t p[t] (vz[t,g] + 8 vs[t,g])
-// so codes enter the products exactly: keys as the binary16 subnormals that an AND
-// leaves of their nibbles (two ANDs and half a shift for two of them), values, whose
-// partner p vs is rounded to 16 bits, around their middle, where that rounding costs a
-// third of what it would around 0 (a packed subtraction more).  The terms of the zeros
-// are one more product each, straight from the words in which scale and zero stand: for the
-// keys against sum(q_g) as two 16-bit values, for the values against p, together with
-// a row of ones that sums p up.  The queries enter exactly, scaled by a power of two of
-// their row's largest value (bf16 ones too: eight bits of eleven).
+// Codes enter the products exactly, as 64 + code, and 64 times their other operand's sum is taken
+// off again.  p vs is rounded to 16 bits; around the middle of the codes that costs a third
+// of what it would around 0, so 8 times the sum of the rounded values is taken off, too (one
+// product with ones for a group).  The terms of the zeros are one more product each, straight
+// from the words in which scale and zero stand: for the keys against sum(q_g) as two 16-bit
+// values, with the scales against -64 of it, for the values against p, together with
+// a row of ones that sums p up.  The queries enter scaled by a power of two of
+// their row's largest value, and so exactly down to 2^-17 of it (2^-28 of it below).
 //
 // A wave takes 16 NQ rows (the query heads of one key/value head, token by token) as
 // the columns of its products and the tokens as the rows: a lane then holds the scores of
@@ -31,34 +31,41 @@ struct AttendArgs {
     bool bf16;
     float scale;                   // softmax scale times log2 e
     int window, sinks;             // window 0: none
-    int splits;                    // parts of a sequence's blocks
-    float *part, *ml;              // [splits][T * q_heads][D] and [..][2], splits > 1
+    int splits, items;             // most parts of a row's blocks; items of all sequences (SHARED)
+    float *part, *ml;              // splits > 1: [splits][T * q_heads][D], and [..][2] maxima and sums
+    int32_t *parts;                // [T * q_heads]: how many of them
 };
 
-constexpr float NONE = -3.0e38f;   // the running maximum before any token
-// A column's maximum is raised only when a score exceeds it by more than this power of
-// two: p <= 4 and p * vs <= 4 * 8736 (a scale is at most 2 * 65504 / 15) stays a
-// binary16, and the rescaling of all accumulators is rare.
+constexpr float NONE = -3.0e38f;   // the reference before any token
+// A column's p are powers of two over a reference that lies `room` under a maximum of its
+// scores, so that small p, and p times the scale of small values, are not lost to the
+// binary16's subnormals.  The reference is raised only when a score exceeds that maximum by
+// more than SLACK, so that rescaling all accumulators is rare.  p <= 2^(room + SLACK)
+// stays a binary16, and so does p * vs for scales up to 2^(13 - room); larger ones take room
+// away, down to -3 for the largest that there are.
 constexpr float SLACK = 2.0f;
+constexpr int ROOM = 13;
 
-// A k-step of a pair of key words: their low (high) nibbles, 2^-24 (2^-20) each.
-__device__ inline half8 code_op(unsigned x, unsigned y, unsigned mask)
+// Codes as operands, 64 + code: the nibble at the exponent of 64, in bits 4 to 7 of a half.  (Left
+// as the subnormals that a mask alone makes of them, or as 1024 + code from bits 0 to 3, they
+// would cost a third fewer instructions; but a product's sums are cut off at 2^-24 or so of its operands'
+// exponents, and a subnormal's is that of 2^-14: measured up to 2^-12 of a code, always to
+// one side, against 2^-16 of this form.)
+constexpr float OFFSET = 64.0f;
+// (no inline assembly: it would not keep the distance to a matrix instruction that reads its result)
+__device__ inline unsigned codes2(unsigned x, unsigned sixty_four) { return (x & 0x00F000F0u) | sixty_four; }
+// a k-step of a pair of key words, of their low or high nibbles
+__device__ inline half8 key_op(unsigned x, unsigned y, bool high, unsigned sixty_four)
 {
-    return __builtin_bit_cast(half8, uint4v{x & mask, x >> 8 & mask, y & mask, y >> 8 & mask});
+    const auto two = [=](unsigned v) { return codes2(v, sixty_four); };
+    return high ? __builtin_bit_cast(half8, uint4v{two(x), two(x >> 8), two(y), two(y >> 8)})
+                : __builtin_bit_cast(half8, uint4v{two(x << 4), two(x >> 4), two(y << 4), two(y >> 4)});
 }
-// The eight codes of a value word, less 8: a low nibble ORed into 0x6400 reads 1024 + v, a
-// high one into 0x5400 64 + v, and the subtraction is exact.
-__device__ inline half8 value_op(unsigned x, unsigned mag_lo, unsigned mag_hi)
+// the eight tokens of a value word, four of each tile
+__device__ inline half8 value_op(unsigned x, unsigned sixty_four)
 {
-    const half2v off_lo = {(_Float16)1032.f, (_Float16)1032.f}, off_hi = {(_Float16)72.f, (_Float16)72.f};
-    const unsigned y = x >> 8;
-    auto lo = [&](unsigned v) {
-        return __builtin_bit_cast(unsigned, __builtin_bit_cast(half2v, and_or_b32(v, 0x000F000Fu, mag_lo)) - off_lo);
-    };
-    auto hi = [&](unsigned v) {
-        return __builtin_bit_cast(unsigned, __builtin_bit_cast(half2v, and_or_b32(v, 0x00F000F0u, mag_hi)) - off_hi);
-    };
-    return __builtin_bit_cast(half8, uint4v{lo(x), lo(y), hi(x), hi(y)});
+    const auto two = [=](unsigned v) { return codes2(v, sixty_four); };
+    return __builtin_bit_cast(half8, uint4v{two(x << 4), two(x >> 4), two(x), two(x >> 8)});
 }
 
 // Whether either half of a word is no finite binary16.
@@ -78,14 +85,35 @@ __device__ inline void wait_loads()
 // A wave's ring of 32-token blocks in LDS.  Loads go there directly: keys and values
 // as they lie, then scales and zeros, [keys | values][group][32] words (repeated up
 // to whole loads of 64 lanes).
-template <int D, int NG>
+template <int D, int NG, int DEPTH>
 struct Ring {
-    static constexpr int STAGES = 2;
+    static constexpr int STAGES = DEPTH;
     static constexpr int CODES = 32 * D / 2;                       // bytes of a block's keys, or of its values
     static constexpr int SCALES = NG > 4 ? 256 * NG : 1024;
     static constexpr int BYTES = 2 * CODES + SCALES;
     static constexpr int LOADS = BYTES / 1024;
 };
+
+// The blocks of tokens that any row at positions p0 .. p1 sees: first the sinks' (0 .. ns - 1), then
+// the window's (from w0 on), nb in all.
+struct SeenBlocks {
+    int ns, w0, nb;
+};
+__device__ inline SeenBlocks seen_blocks(int p0, int p1, int window, int sinks, int cap)
+{
+    SeenBlocks r = {0, 0, 0};
+    const int end = p1 < cap ? p1 : cap - 1;
+    if (end < 0) return r;
+    if (window) {
+        const int from = p0 - window + 1;
+        r.w0 = from > 0 ? from >> 5 : 0;
+        if (r.w0 > end >> 5) r.w0 = (end >> 5) + 1;
+        r.ns = (sinks + 31) >> 5;
+        r.ns = r.ns < r.w0 ? r.ns : r.w0;
+    }
+    r.nb = r.ns + (end >> 5) - r.w0 + 1;
+    return r;
+}
 
 // MERGE: the workgroup's four waves share 16 NQ rows and take every fourth block of
 // tokens; their results meet in LDS at the end.  Otherwise each wave has rows of its own.
@@ -94,7 +122,7 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
 {
     constexpr int NW = D / 32, DT = D / 16, SPG = NW / NG, TPG = DT / NG;
     constexpr int ROWS = 16 * NQ, RB = MERGE ? ROWS : 4 * ROWS;
-    using RG = Ring<D, NG>;
+    using RG = Ring<D, NG, 2>;
     constexpr int LD = D + 4;                              // (a row of the waves' results)
     constexpr int RINGS = 4 * RG::STAGES * RG::BYTES, SUMS = MERGE ? 4 * 16 * (LD + 2) * 4 : 0;
     // (one array for all: with several the compiler puts a wait for all loads before each
@@ -104,11 +132,48 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
     const int col = lane & 15, kq = lane >> 4;
     const int H = c.heads, R = a.R;
     uint8_t *const ring = lds + w * (RG::STAGES * RG::BYTES);
+    const int cap = s.width << c.shift;                    // tokens that the table has room for
     const int h = blockIdx.x % H, xs = blockIdx.x / H;
-    const int split = xs % a.splits;
-    int b, in, of;
+    // the rows' block, and the part of the tokens
+    const auto row_blocks = [=](const Run &q) { return (q.n * R + RB - 1) / RB; };
+    int b, in, of, split = 0, part_blocks = 0;
     Run seq;
-    if (!kv4_find(s, xs / a.splits, [=](const Run &q) { return (q.n * R + RB - 1) / RB; }, b, in, of, seq)) return;
+    if (MERGE && a.splits > 1) {
+        // Parts of one size for all sequences, the longest that a.items of them cover all
+        // tokens with: a sequence's last one may be shorter, so as many as there are row blocks are
+        // kept back.  (Every wave counts for itself, 64 sequences a step.)
+        const auto blocks_of = [=](const Run &q) { return seen_blocks(q.len - q.n, q.len - 1, a.window, a.sinks, cap).nb; };
+        long long total = 0;
+        int rbs = 0;
+        bool huge = false;
+        const Run head = kv4_seq(s, lane);                 // (of up to 64 sequences the only load)
+        const auto run = [&](int i) { return i < 64 ? head : kv4_seq(s, i); };
+        for (int b0 = 0; b0 < s.B; b0 += 64) {
+            const Run q = run(b0 + lane);
+            const int r = q.n > 0 ? row_blocks(q) : 0, nb1 = r > 0 ? blocks_of(q) : 0;
+            huge |= __any((long long)r * nb1 >= 1 << 24);
+            total += __builtin_amdgcn_readlane(scan64(huge ? 0 : r * nb1), 63);
+            rbs += __builtin_amdgcn_readlane(scan64(r), 63);
+        }
+        const int spare = a.items - rbs;
+        part_blocks = 1 << 28;                             // (too many to count, or no room: no parts)
+        if (!huge && total < 1 << 30 && spare > 0)
+            part_blocks = (((unsigned)total + spare - 1) / (unsigned)spare + 4) & ~3u;
+        const auto parts_of = [=](const Run &q) {
+            const int n = (int)((unsigned)(blocks_of(q) + part_blocks - 1) / (unsigned)part_blocks);
+            return n < 1 ? 1 : n < a.splits ? n : a.splits;
+        };
+        if (!find_item(s.B, xs, run, [&](const Run &q) { return row_blocks(q) * parts_of(q); }, b, in, of, seq)) return;
+        const int n = parts_of(seq);
+        part_blocks = ((blocks_of(seq) + n - 1) / n + 3) & ~3;
+        split = in % n;
+        in /= n;
+        of /= n;
+    } else {
+        split = xs % a.splits;
+        if (!kv4_find(s, xs / a.splits, row_blocks, b, in, of, seq)) return;
+    }
+    b = __builtin_amdgcn_readfirstlane(b);                 // (the compiler does not see that it is one)
     in = of - 1 - in;                                      // the longest first
     const int rows = seq.n * R;
     const int row0 = in * RB + (MERGE ? 0 : w * ROWS);
@@ -117,23 +182,11 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
     const int first = seq.len - seq.n;                     // position of the first row's token
     const int p0 = first + row0 / R, p1 = first + last / R;
 
-    // the blocks of tokens that any of the rows sees: the sinks', then the window's
-    const int cap = s.width << c.shift;
-    const int end = p1 < cap ? p1 : cap - 1;
-    int ns = 0, w0 = 0, nb = 0;
-    if (end >= 0) {
-        if (a.window) {
-            const int from = p0 - a.window + 1;
-            w0 = from > 0 ? from >> 5 : 0;
-            ns = (a.sinks + 31) >> 5;
-            if (w0 > end >> 5) w0 = (end >> 5) + 1;
-            ns = ns < w0 ? ns : w0;
-        }
-        nb = ns + (end >> 5) - w0 + 1;
-    }
+    const SeenBlocks seen = seen_blocks(p0, p1, a.window, a.sinks, cap);
+    const int ns = seen.ns, w0 = seen.w0, nb = seen.nb;
     int per = (nb + a.splits - 1) / a.splits;
-    if (MERGE) per = (per + 3) & ~3;
-    const int j0 = split * per, j1 = j0 + per < nb ? j0 + per : nb;
+    if (MERGE) per = a.splits > 1 ? part_blocks : nb;      // (a row block sees no more than its sequence)
+    const int j0 = split * per < nb ? split * per : nb, j1 = j0 + per < nb ? j0 + per : nb;
     const int step = MERGE ? 4 : 1;
 
     // the rows' queries, and positions
@@ -159,7 +212,11 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
         const int j = j0 + (MERGE ? w : 0) + i * step;
         return j < ns ? j : j - ns + w0;
     };
-    auto page_of = [&](int i) { return s.table[(size_t)b * s.width + (block_of(i) >> (c.shift - 5))]; };
+    // (from the constant address space, for a scalar load: a vector load's wait would be one for
+    // the blocks asked for before it, too)
+    const __attribute__((address_space(4))) int32_t *const pages =
+        (const __attribute__((address_space(4))) int32_t *)(uintptr_t)(s.table + (size_t)b * s.width);
+    auto page_of = [&](int i) { return pages[block_of(i) >> (c.shift - 5)]; };
     constexpr int SLOADS = RG::SCALES / 1024;
     const uint32_t *sz0[SLOADS];
 #pragma unroll
@@ -173,25 +230,34 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
         const size_t at = ((head << c.shift) + tin) * (D / 8);
         uint8_t *const to = ring + (i % RG::STAGES) * RG::BYTES;
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u) lds_load16<0>(c.k + at + u * 256 + lane * 4, to + u * 1024);
+        for (int u = 0; u < D / 64; ++u) lds_load16<MERGE ? QG_NT : 0>(c.k + at + u * 256 + lane * 4, to + u * 1024);
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u) lds_load16<0>(c.v + at + u * 256 + lane * 4, to + RG::CODES + u * 1024);
+        for (int u = 0; u < D / 64; ++u) lds_load16<MERGE ? QG_NT : 0>(c.v + at + u * 256 + lane * 4, to + RG::CODES + u * 1024);
         const size_t sat = ((head * NG) << c.shift) + tin;
 #pragma unroll
-        for (int u = 0; u < SLOADS; ++u) lds_load16<0>(sz0[u] + sat, to + 2 * RG::CODES + u * 1024);
+        for (int u = 0; u < SLOADS; ++u) lds_load16<MERGE ? QG_NT : 0>(sz0[u] + sat, to + 2 * RG::CODES + u * 1024);
     };
 
-    // pages are asked for two blocks ahead, blocks one
-    int pg = 0, next = 0;
+    // the first blocks; a bit for each in flight says whether it has a page
+    constexpr int AHEAD = RG::STAGES - 1;
+    unsigned has = 0;
+    int next = 0;                                          // the page of the block to be asked for next
     if (mine > 0) {
-        pg = page_of(0);
-        next = page_of(mine > 1 ? 1 : 0);
-        load(0, pg);
+        int pg[AHEAD];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) pg[i] = page_of(i < mine ? i : 0);
+        next = page_of(AHEAD < mine ? AHEAD : 0);
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (i < mine) {
+                has |= ((unsigned)pg[i] < (unsigned)c.pages ? 1u : 0u) << i;
+                load(i, pg[i]);
+            }
     }
 
-    // the queries as operands, q' = q 2^(15 - ex) below 2^15 (sixteenths against the high
-    // nibbles); the factor of the scores (the codes weigh 2^-24); the groups' sums as two
-    // 16-bit values, against the zeros in the words of lane groups 0 (the upper part) and 1
+    // the queries as operands, q' = q 2^(3 - ex) below 8 (64 times their sum is a binary16
+    // still); the factor of the scores; the groups' sums as two 16-bit values, against the zeros
+    // in the words of lane groups 0 (the upper part) and 1, and -64 times these against the scales
     half8 qo[NQ][NW], qz[NQ];
     float f[NQ];
     constexpr int GL = NG > 4 ? 2 : 1;                     // lane groups that the groups' words take
@@ -216,7 +282,7 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
         bad |= __shfl_xor((int)bad, 32) != 0;
         int ex = 0;
         if (big > 0.0f && !bad) (void)frexpf(big, &ex);    // big < 2^ex
-        f[n] = bad ? __builtin_nanf("") : ldexpf(a.scale, ex + 9);
+        f[n] = bad ? __builtin_nanf("") : ldexpf(a.scale, ex - 3);
         float qs[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -225,13 +291,13 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
             for (int k = g * SPG; k < (g + 1) * SPG; ++k)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[k][e] = ldexpf(x[k][e], 15 - ex);
+                    x[k][e] = ldexpf(x[k][e], 3 - ex);
                     sum += x[k][e];
-                    qo[n][k][e] = (_Float16)(k < NW / 2 ? x[k][e] : 0.0625f * x[k][e]);
+                    qo[n][k][e] = (_Float16)x[k][e];
                 }
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
-            qs[g] = sum * 0x1p-24f;
+            qs[g] = sum;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -242,13 +308,13 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
                 v = qs[i];
             const _Float16 hi = (_Float16)v;
             const _Float16 part = kq / GL == 0 ? hi : kq / GL == 1 ? (_Float16)(v - (float)hi) : (_Float16)0.0f;
-            qz[n][2 * i] = (_Float16)0.0f;
+            qz[n][2 * i] = (_Float16)(-OFFSET * (float)part);
             qz[n][2 * i + 1] = part;
         }
     }
 
-    // running maximum; products with the values' codes; with their scales (even rows) and
-    // zeros (odd), and with ones (row 2 NG: the sum of p; with eight groups no row is left)
+    // references; products with the values' codes; with their scales (even rows) and zeros
+    // (odd), and with ones (row 2 NG: the sum of p; with eight groups no row is left)
     constexpr bool LROW = 2 * NG < 16;
     float m[NQ], l[NQ];
     float4v o[NQ][DT], z[NQ];
@@ -260,56 +326,90 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[n][d] = float4v{0, 0, 0, 0};
     }
-    unsigned mag_lo = 0x64006400u, mag_hi = 0x54005400u;
-    pin(mag_lo);
-    pin(mag_hi);
+    // group g's sum of p vs: row MROW + g, of the same accumulator where there is room
+    constexpr int MROW = LROW ? 2 * NG + 1 : 0;
+    float4v mid[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) mid[n] = float4v{0, 0, 0, 0};
+    int room = ROOM;
+    unsigned sixty_four = 0x54005400u;
+    asm("" : "+v"(sixty_four));                            // (a register: an instruction takes one constant)
 
     auto block = [&](const uint8_t *x, int t0, bool ok) {
+        int ln = lane;                                     // (of many groups: what comes from it is not kept in
+        if (NG > 2) asm("" : "+v"(ln));                    // registers)
+        const int col = ln & 15, kq = ln >> 4, lane = ln;
         const uint4v *const ksz = reinterpret_cast<const uint4v *>(x + 2 * RG::CODES) + kq;
         const uint4v *const vsz = ksz + NG * 8;
         const unsigned *const kw = reinterpret_cast<const unsigned *>(x + 2 * RG::CODES) + col;
+        // the keys' words, and their scales and zeros, all at once
+        constexpr bool EARLY = NG * NQ <= 2;               // (more scales and zeros are read when needed)
+        constexpr bool EARLY_V = NG * NQ <= 1;
+        uint4v kr[2][(NW + 3) / 4], zw[2], sk[2][NG];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const uint8_t *const kt = x + t * (RG::CODES / 2) + (col * 4 + kq) * (D / 8);
+            if constexpr (NW == 2) {
+                const uint2v r2 = *reinterpret_cast<const uint2v *>(kt);
+                kr[t][0] = uint4v{r2.x, r2.y, 0, 0};
+            } else {
+#pragma unroll
+                for (int i = 0; i < NW / 4; ++i) kr[t][i] = *reinterpret_cast<const uint4v *>(kt + 16 * i);
+            }
+            zw[t] = uint4v{0, 0, 0, 0};                    // this lane's token: (scale, zero) of four groups
+#pragma unroll
+            for (int i = 0; i < (NG < 4 ? NG : 4); ++i)
+                zw[t][i] = kw[(NG > 4 ? (kq & 1) * 4 + i : i) * 32 + 16 * t];
+#pragma unroll
+            for (int g = 0; g < (EARLY ? NG : 0); ++g) sk[t][g] = ksz[g * 8 + t * 4];
+        }
+        __builtin_amdgcn_sched_barrier(0);                 // (not each where it is needed, with a wait of its own)
         float4v sc[NQ][2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            half8 op[NW];
-            const uint8_t *const kt = x + t * (RG::CODES / 2) + (col * 4 + kq) * (D / 8);
-#pragma unroll
-            for (int i = 0; i < NW / 2; i += 2) {
-                uint4v r = {0, 0, 0, 0};
-                if constexpr (NW == 2) {
-                    const uint2v r2 = *reinterpret_cast<const uint2v *>(kt);
-                    r.x = r2.x;
-                    r.y = r2.y;
-                } else {
-                    r = *reinterpret_cast<const uint4v *>(kt + 8 * i);
-                }
-                op[i] = code_op(r.x, r.y, 0x000F000Fu);
-                op[i + NW / 2] = code_op(r.x, r.y, 0x00F000F0u);
-                if constexpr (NW > 2) {
-                    op[i + 1] = code_op(r.z, r.w, 0x000F000Fu);
-                    op[i + 1 + NW / 2] = code_op(r.z, r.w, 0x00F000F0u);
-                }
-            }
-            uint4v zw = {0, 0, 0, 0};                      // this lane's token: (scale, zero) of four groups
-#pragma unroll
-            for (int i = 0; i < (NG < 4 ? NG : 4); ++i)
-                zw[i] = kw[(NG > 4 ? (kq & 1) * 4 + i : i) * 32 + 16 * t];
+            const auto op = [&](int k) {
+                const uint4v r = kr[t][k % (NW / 2) / 2];
+                return k % (NW / 2) & 1 ? key_op(r.z, r.w, k >= NW / 2, sixty_four) : key_op(r.x, r.y, k >= NW / 2, sixty_four);
+            };
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
-                sc[n][t] = mfma_f16(__builtin_bit_cast(half8, zw), qz[n], float4v{0, 0, 0, 0});
+                sc[n][t] = mfma_f16(__builtin_bit_cast(half8, zw[t]), qz[n], float4v{0, 0, 0, 0});
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const uint4v sz = ksz[g * 8 + t * 4];
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    float4v acc = {0, 0, 0, 0};
-#pragma unroll
-                    for (int k = g * SPG; k < (g + 1) * SPG; ++k) acc = mfma_f16(op[k], qo[n][k], acc);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) sc[n][t][r] = __builtin_fmaf(lo16(sz[r]), acc[r], sc[n][t][r]);
+                if (!EARLY) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    sk[t][g] = ksz[g * 8 + t * 4];
                 }
+                float4v acc[NQ];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) acc[n] = float4v{0, 0, 0, 0};
+#pragma unroll
+                for (int k = g * SPG; k < (g + 1) * SPG; ++k) {
+                    const half8 kc = op(k);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) acc[n] = mfma_f16(kc, qo[n][k], acc[n]);
+                }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sc[n][t][r] = __builtin_fmaf(lo16(sk[t][g][r]), acc[n][r], sc[n][t][r]);
             }
         }
+        // the values' words, scales and zeros, on their way while the softmax is taken; za: those of
+        // a row of the zeros' product, of which lane (col, kq) takes the halves of one kind of
+        // group col / 2, of the eight tokens of lane group kq
+        const int zg = col / 2 < NG ? col / 2 : 0;
+        const auto values = [&](int u) { return *reinterpret_cast<const uint4v *>(x + RG::CODES + u * 1024 + lane * 16); };
+        uint4v vr[D / 64], sv[2][NG], za[2];
+#pragma unroll
+        for (int u = 0; u < (EARLY ? D / 64 : 0); ++u) vr[u] = values(u);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int g = 0; g < (EARLY_V ? NG : 0); ++g) sv[t][g] = vsz[g * 8 + t * 4];
+            za[t] = vsz[zg * 8 + t * 4];
+        }
+        __builtin_amdgcn_sched_barrier(0);
         // all rows see all of the block, or some do not: a bit for each score that is hidden
         const bool whole = ok && t0 + 31 <= p0 && (!a.window || t0 > p1 - a.window || t0 + 31 < a.sinks);
         unsigned hide[NQ];
@@ -328,24 +428,54 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
                     }
             }
         }
-        bool raise = false;
+        if (!whole) {
+            // a token that one row sees and another does not must not bring it a NaN: 0 here, and a NaN
+            // put in where it is seen; one that no row sees counts for nothing
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = t0 + 16 * t + 4 * kq + r;
+                    const bool some = ok && at <= p1 && (!a.window || at > p0 - a.window || at < a.sinks);
+                    za[t][r] = !some || odd_word(za[t][r]) ? 0u : za[t][r];
+                }
+        }
+        // the largest of the scales, over all groups and tokens in one lane or another
+        typedef unsigned short ushort2v __attribute__((ext_vector_type(2)));
+        ushort2v large = __builtin_bit_cast(ushort2v, za[0][0]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) large = __builtin_elementwise_max(large, __builtin_bit_cast(ushort2v, za[i / 4][i % 4]));
+        bool raise = room > -3 && large.x > (unsigned)(28 - room) << 10;
+        float less = 0.0f;
+        if (__any(raise)) {
+            int e = large.x >> 10;                         // vs < 2^(e - 14)
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int other = __shfl_xor(e, o);
+                e = other > e ? other : e;
+            }
+            const int now = 27 - e > -3 ? 27 - e : -3;
+            less = (float)(room - now);
+            room = now;
+        }
         float mx[NQ];
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             float v = fmaxf(fmaxf(sc[n][0][0], sc[n][0][1]), fmaxf(sc[n][0][2], sc[n][0][3]));
             v = fmaxf(v, fmaxf(fmaxf(sc[n][1][0], sc[n][1][1]), fmaxf(sc[n][1][2], sc[n][1][3])));
             mx[n] = v * f[n];                              // (f > 0)
-            raise |= mx[n] > m[n] + SLACK;
+            raise |= mx[n] > m[n] + (SLACK + (float)room);
         }
         if (__any(raise)) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
                 float v = fmaxf(mx[n], __shfl_xor(mx[n], 16));
-                v = fmaxf(m[n], fmaxf(v, __shfl_xor(v, 32)));
+                v = fmaxf(m[n] + less, fmaxf(v, __shfl_xor(v, 32)) - (float)room);
                 const float by = __builtin_amdgcn_exp2f(m[n] - v);
                 m[n] = v;
                 l[n] *= by;
                 z[n] *= by;
+                if (!LROW) mid[n] *= by;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[n][d] *= by;
             }
@@ -377,35 +507,26 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
                     if (!LROW) l[n] += sc[n][t][r];
                 }
 
-        // the rows of scales and zeros: lane (col, kq) takes the halves of one kind of group
-        // col / 2, of the eight tokens of lane group kq
-        const int zg = col / 2 < NG ? col / 2 : 0;
-        uint4v za[2], zh;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) za[t] = vsz[zg * 8 + t * 4];
-        if (!whole) {
-            // a token that one row sees and another does not must not bring it a NaN: 0 here, and a NaN
-            // put in where it is seen
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) za[t][r] = odd_word(za[t][r]) ? 0u : za[t][r];
-        }
+        uint4v zh;
         const unsigned sel = (col & 1) ? 0x07060302u : 0x05040100u;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             zh[2 * t] = __builtin_amdgcn_perm(za[t][1], za[t][0], sel);
             zh[2 * t + 1] = __builtin_amdgcn_perm(za[t][3], za[t][2], sel);
         }
-        if (LROW && col >= 2 * NG) zh = uint4v{0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+        if (LROW && col >= 2 * NG) {                       // (rows behind that of the ones: nothing)
+            const unsigned w1 = col == 2 * NG ? 0x3C003C00u : 0u;
+            zh = uint4v{w1, w1, w1, w1};
+        }
 #pragma unroll
         for (int n = 0; n < NQ; ++n) z[n] = mfma_f16(__builtin_bit_cast(half8, zh), pf[n], z[n]);
 
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             uint4v sz[2];
+            if (!EARLY_V) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) sz[t] = vsz[g * 8 + t * 4];
+            for (int t = 0; t < 2; ++t) sz[t] = EARLY_V ? sv[t][g] : vsz[g * 8 + t * 4];
             if (!whole) {
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
@@ -426,6 +547,9 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
 #pragma unroll
                     for (int r = 0; r < 4; ++r) sz[t][r] = odd_word(sz[t][r]) ? 0u : sz[t][r];
             }
+            if (!EARLY)
+#pragma unroll
+                for (int u = (g * TPG + 3) / 4; u < ((g + 1) * TPG + 3) / 4; ++u) vr[u] = values(u);
             half8 po[NQ];
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
@@ -433,10 +557,16 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) po[n][4 * t + r] = (_Float16)__builtin_fmaf(lo16(sz[t][r]), sc[n][t][r], 0.0f);
+            const unsigned one = col == MROW + g ? 0x3C003C00u : 0u;
+            const half8 ones = __builtin_bit_cast(half8, uint4v{one, one, one, one});
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                float4v &to = LROW ? z[n] : mid[n];
+                to = mfma_f16(ones, po[n], to);
+            }
 #pragma unroll
             for (int d = g * TPG; d < (g + 1) * TPG; ++d) {
-                const half8 vo = value_op(*reinterpret_cast<const unsigned *>(x + RG::CODES + d / 4 * 1024 + lane * 16 + d % 4 * 4),
-                                          mag_lo, mag_hi);
+                const half8 vo = value_op(vr[d / 4][d % 4], sixty_four);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) o[n][d] = mfma_f16(vo, po[n], o[n][d]);
             }
@@ -444,18 +574,24 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
     };
 
     for (int i = 0; i < mine; ++i) {
-        const int here = pg;
-        pg = next;
-        if (i + 1 < mine) {
-            next = page_of(i + 2 < mine ? i + 2 : i + 1);
+        const int more = mine - 1 - i;                     // blocks behind this one
+        if (more >= AHEAD) {
+            has |= ((unsigned)next < (unsigned)c.pages ? 1u : 0u) << AHEAD;
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage's last reads are done
-            load(i + 1, pg);
+            load(i + AHEAD, next);
             debug_stage_sync();
+            wait_loads<AHEAD * RG::LOADS>();
+            __builtin_amdgcn_sched_barrier(0);             // (behind that wait, or it waits for this load)
+            next = page_of(more > AHEAD ? i + AHEAD + 1 : i);
+        } else if (AHEAD > 2 && more == 2) {
+            wait_loads<2 * RG::LOADS>();
+        } else if (AHEAD > 1 && more == 1) {
             wait_loads<RG::LOADS>();
         } else {
             wait_loads<0>();
         }
-        block(ring + (i % RG::STAGES) * RG::BYTES, block_of(i) << 5, (unsigned)here < (unsigned)c.pages);
+        block(ring + (i % RG::STAGES) * RG::BYTES, block_of(i) << 5, (has & 1u) != 0);
+        has >>= 1;
     }
 
     // a column's sum of p, and its values with the zeros' part, from the lane groups that hold them
@@ -470,9 +606,12 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
         const float zz[2] = {__builtin_fmaf(z[n][0], 8.0f, z[n][1]), __builtin_fmaf(z[n][2], 8.0f, z[n][3])};
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const float zs = __shfl(zz[g % 2], 16 * (g / 2) + col);
+            const float zs = __shfl(zz[g % 2], 16 * (g / 2) + col) -
+                             (OFFSET + 8.0f) * __shfl((LROW ? z : mid)[n][(MROW + g) % 4], 16 * ((MROW + g) / 4) + col);
 #pragma unroll
-            for (int d = g * TPG; d < (g + 1) * TPG; ++d) o[n][d] += zs;
+            for (int d = g * TPG; d < (g + 1) * TPG; ++d)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[n][d][r] += zs;
         }
     }
 
@@ -509,6 +648,7 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
                 const int rr = row0 + 16 * n + r, i = rr / R;
                 const size_t g = ((size_t)seq.row + i) * a.q_heads + (size_t)h * R + (rr - i * R);
                 if (a.splits > 1) {
+                    if (ch == 0 && split == 0) a.parts[g] = per < nb ? (nb + per - 1) / per : 1;
                     if (ch == 0) {
                         a.ml[(split * all + g) * 2] = mm;
                         a.ml[(split * all + g) * 2 + 1] = sum;
@@ -532,6 +672,7 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
             if (row0 + 16 * n + col >= rows) continue;
             if (a.splits > 1) {
                 if (kq == 0) {
+                    if (split == 0) a.parts[grow[n]] = a.splits;
                     a.ml[(split * all + grow[n]) * 2] = m[n];
                     a.ml[(split * all + grow[n]) * 2 + 1] = l[n];
                 }
@@ -559,9 +700,9 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
 // without a token hold sum 0 and no values.
 constexpr int MAX_SPLITS = 128;
 template <int D>
-__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Batch s, AttendArgs a)
+__global__ __launch_bounds__(512) void kv4_join_kernel(Kv4Batch s, AttendArgs a)
 {
-    constexpr int TPR = D / 4, GR = 256 / TPR;
+    constexpr int TPR = D / 4, GR = 512 / TPR, MOST = (MAX_SPLITS + GR - 1) / GR;
     const size_t all = (size_t)s.T * a.q_heads, g = blockIdx.x;
     if (s.off) {                                          // rows of no sequence stay as they are
         const long long t = (long long)(g / a.q_heads);
@@ -570,11 +711,19 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Batch s, AttendArgs a)
     const int tid = threadIdx.x, grp = tid / TPR, ch = tid % TPR * 4;
     __shared__ float4v so[GR][TPR];
     __shared__ float by[MAX_SPLITS], top[2], total[2];
+    int n = a.parts[g];
+    n = n < 0 ? 0 : n < a.splits ? n : a.splits;
     // (two waves hold the parts)
     float mi = NONE, li = 0.0f;
-    if (tid < a.splits) {
+    if (tid < n) {
         mi = a.ml[(tid * all + g) * 2];
         li = a.ml[(tid * all + g) * 2 + 1];
+    }
+    float4v v[MOST];
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+        const int k = grp + i * GR;                        // (past the last: read again, weight 0)
+        v[i] = *reinterpret_cast<const float4v *>(a.part + ((k < n ? k : 0) * all + g) * D + ch);
     }
     float m = mi;
 #pragma unroll
@@ -595,10 +744,11 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Batch s, AttendArgs a)
     debug_stage_sync();
     __syncthreads();
     float4v acc = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int i = grp; i < a.splits; i += GR) {
-        const float e = by[i];
-        if (e != 0.0f) acc += e * *reinterpret_cast<const float4v *>(a.part + (i * all + g) * D + ch);
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+        const int k = grp + i * GR;
+        const float e = k < MAX_SPLITS ? by[k] : 0.0f;
+        if (e != 0.0f) acc += e * v[i];
     }
     so[grp][tid % TPR] = acc;
     debug_stage_sync();
@@ -608,10 +758,10 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4Batch s, AttendArgs a)
     for (int i = 1; i < GR; ++i) acc += so[i][tid];
     const float sum = total[0] + total[1];
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t v[4];
+    uint16_t r[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = a.bf16 ? f2bf(acc[e] * inv) : f2h(acc[e] * inv);
-    *reinterpret_cast<uint2v *>(a.out + g * D + ch) = uint2v{v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16};
+    for (int e = 0; e < 4; ++e) r[e] = a.bf16 ? f2bf(acc[e] * inv) : f2h(acc[e] * inv);
+    *reinterpret_cast<uint2v *>(a.out + g * D + ch) = uint2v{r[0] | (uint32_t)r[1] << 16, r[2] | (uint32_t)r[3] << 16};
 }
 
 template <int D, int NG>
@@ -647,15 +797,35 @@ Kv4AttendPlan kv4_attend_plan(int T, int max_new, int B, int q_heads, int heads,
         const long long seen = (long long)window + sinks + max_new + 64;
         tokens = seen < tokens ? seen : tokens;
     }
-    // parts along the tokens fill the CUs once (three workgroups each of 64 or 128 shared
-    // channels, else two), of at least a block of tokens for each wave
+    // Parts along the tokens where the rows alone do not fill the CUs once (with three workgroups
+    // each of shared rows up to 128 channels, else two), of at least a block of tokens for each
+    // wave.  Rows that a workgroup's waves share are cut into parts of one size (the kernel
+    // finds it), the others each into as many.
     const long long most = (tokens + 127) / 128, fit = p.shared && D < 256 ? 768 : 512;
-    long long n = fit / likely;
-    n = n > most ? most : n;
-    n = n > MAX_SPLITS ? MAX_SPLITS : n;
-    p.splits = n < 1 ? 1 : (int)n;
-    p.workgroups = blocks * heads * p.splits;
-    p.bytes = p.splits == 1 ? 0 : (size_t)p.splits * T * q_heads * (D + 2) * sizeof(float);
+    p.splits = 1;
+    p.items = 0;
+    if (p.shared) {
+        long long n = fit / heads;
+        n = n < some * most ? n : some * most;
+        // (joining them costs 5 us: not for fewer than two parts each of few tokens; 64 sequences
+        // that see 1000 tokens each take 36 us in 96 parts, 29 whole.  Of many tokens a
+        // sequence may be far longer than the others.)
+        if (n >= 2 * some || (n > some && tokens > 4096)) {
+            p.items = (int)n;
+            n = n - some + 1;
+            p.splits = (int)(n < MAX_SPLITS ? n : MAX_SPLITS);
+            // (no part may be numbered past them: fewer items, longer parts)
+            if (p.items > p.splits + some - 1) p.items = (int)(p.splits + some - 1);
+        }
+        if (p.splits == 1) p.items = 0;
+    } else {
+        long long n = fit / likely;
+        n = n > most ? most : n;
+        n = n > MAX_SPLITS ? MAX_SPLITS : n;
+        p.splits = n < 1 ? 1 : (int)n;
+    }
+    p.workgroups = (p.items ? (p.items > blocks ? p.items : blocks) : blocks * p.splits) * heads;
+    p.bytes = p.splits == 1 ? 0 : (size_t)T * q_heads * ((size_t)p.splits * (D + 2) + 1) * sizeof(float);
     return p;
 }
 
@@ -666,8 +836,9 @@ hipError_t launch_kv4_attend(const Kv4AttendPlan &p, const Kv4Cache &c, const Kv
     const size_t all = (size_t)s.T * q_heads;
     float *const part = (float *)ws;
     const AttendArgs a = {(const uint16_t *)q, (uint16_t *)out, ldq, q_heads, q_heads / c.heads, dtype == QG_DT_BF16,
-                          scale * 1.4426950408889634f, window, sinks, p.splits, part,
-                          part ? part + (size_t)p.splits * all * c.D : nullptr};
+                          scale * 1.4426950408889634f, window, sinks, p.splits, p.items, part,
+                          part ? part + (size_t)p.splits * all * c.D : nullptr,
+                          part ? (int32_t *)(part + (size_t)p.splits * all * (c.D + 2)) : nullptr};
     const int ng = c.D / c.g;
 #define QG_ATTEND(DIM, GROUPS) \
     if (c.D == DIM && ng == GROUPS) launch_attend<DIM, GROUPS>(p, c, s, a, st)
@@ -684,9 +855,9 @@ hipError_t launch_kv4_attend(const Kv4AttendPlan &p, const Kv4Cache &c, const Kv
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     switch (c.D) {
-    case 64: hipLaunchKernelGGL((kv4_join_kernel<64>), dim3((unsigned)all), dim3(256), 0, st, s, a); break;
-    case 128: hipLaunchKernelGGL((kv4_join_kernel<128>), dim3((unsigned)all), dim3(256), 0, st, s, a); break;
-    default: hipLaunchKernelGGL((kv4_join_kernel<256>), dim3((unsigned)all), dim3(256), 0, st, s, a); break;
+    case 64: hipLaunchKernelGGL((kv4_join_kernel<64>), dim3((unsigned)all), dim3(512), 0, st, s, a); break;
+    case 128: hipLaunchKernelGGL((kv4_join_kernel<128>), dim3((unsigned)all), dim3(512), 0, st, s, a); break;
+    default: hipLaunchKernelGGL((kv4_join_kernel<256>), dim3((unsigned)all), dim3(512), 0, st, s, a); break;
     }
     return hipGetLastError();
 }

@@ -184,7 +184,7 @@ hipError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &s, int dtype, void
 // a wave, parts along the tokens, workgroups, bytes of workspace.
 struct Kv4AttendPlan {
     bool shared;
-    int rows, splits;
+    int rows, splits, items;       // items (shared rows): parts of all rows of a key/value head
     long long workgroups;
     size_t bytes;
 };

@@ -96,7 +96,7 @@ def test_attend_workspace_sizes():
     bad = ctypes.c_size_t(-1).value
     assert f(0, 1, 4, 8, 2, 128, 4, 64, 0, 0) == 0
     n = f(1, 1, 1, 8, 8, 128, 2048, 64, 0, 0)
-    assert n > 0 and n % (8 * 130 * 4) == 0                       # parts of 8 rows of 128 values, maximum and sum
+    assert n > 8 * 130 * 4 and n % (8 * 4) == 0                   # parts of 8 rows of 128 values, maximum and sum; their number
     assert f(1, 1, 1, 8, 8, 128, 2048, 64, 128, 0) < n            # a window needs fewer
     assert f(4096, 4096, 1, 64, 8, 128, 2048, 64, 0, 0) == 0      # enough rows: no parts
     for args in ((-1, 1, 1, 8, 8, 128, 4, 64, 0, 0), (1, 0, 1, 8, 8, 128, 4, 64, 0, 0), (1, 1, 1, 8, 3, 128, 4, 64, 0, 0),
