@@ -547,7 +547,7 @@ int kv4_attend(const void *q, int dtype, int T, int ld_q, int q_heads, int max_n
  * type.  Y must not overlap the other tensors.
  * workspace  qg_workspace_bytes(QG_OP_LORA, T, N, K, R, L, 0) bytes, 256-byte
  *          aligned; nothing is kept in it between calls.  T == 0 does nothing.
- *          Two kernels.                                                      */
+ *          Two kernels, or three where adapters have many rows each.         */
 int lora_add(const void *X, const void *A, const void *B, const float *scaling,
              const int32_t *adapter_offsets, const int32_t *row_token, const int32_t *slot_row,
              int L, int T, int K, int N, int R, int dtype, void *Y, void *workspace,
