@@ -115,16 +115,18 @@ __device__ inline SeenBlocks seen_blocks(int p0, int p1, int window, int sinks, 
     return r;
 }
 
-// MERGE: the workgroup's four waves share 16 NQ rows and take every fourth block of
-// tokens; their results meet in LDS at the end.  Otherwise each wave has rows of its own.
-template <int D, int NG, int NQ, bool MERGE>
-__global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s, AttendArgs a)
+// SHARE 4 or 8: the workgroup's waves, as many, share 16 NQ rows and take every SHARE-th block
+// of tokens; their results meet in LDS at the end.  SHARE 1: each of four has rows of its own.
+template <int D, int NG, int NQ, int SHARE>
+__global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 : 2) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s, AttendArgs a)
 {
     constexpr int NW = D / 32, DT = D / 16, SPG = NW / NG, TPG = DT / NG;
+    constexpr bool MERGE = SHARE > 1;
+    constexpr int WAVES = MERGE ? SHARE : 4;
     constexpr int ROWS = 16 * NQ, RB = MERGE ? ROWS : 4 * ROWS;
     using RG = Ring<D, NG, 2>;
     constexpr int LD = D + 4;                              // (a row of the waves' results)
-    constexpr int RINGS = 4 * RG::STAGES * RG::BYTES, SUMS = MERGE ? 4 * 16 * (LD + 2) * 4 : 0;
+    constexpr int RINGS = WAVES * RG::STAGES * RG::BYTES, SUMS = MERGE ? WAVES * 16 * (LD + 2) * 4 : 0;
     // (one array for all: with several the compiler puts a wait for all loads before each
     // read of the ring)
     __shared__ __attribute__((aligned(16))) uint8_t lds[RINGS > SUMS ? RINGS : SUMS];
@@ -187,7 +189,6 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
     int per = (nb + a.splits - 1) / a.splits;
     if (MERGE) per = a.splits > 1 ? part_blocks : nb;      // (a row block sees no more than its sequence)
     const int j0 = split * per < nb ? split * per : nb, j1 = j0 + per < nb ? j0 + per : nb;
-    const int step = MERGE ? 4 : 1;
 
     // the rows' queries, and positions
     uint4v raw[NQ][NW];
@@ -206,10 +207,10 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
         for (int k = 0; k < NW; ++k) raw[n][k] = *reinterpret_cast<const uint4v *>(p + 32 * k);
     }
 
-    // a wave's blocks: every `step`-th from j0 + (its number) on
-    const int mine = j1 <= j0 ? 0 : (MERGE ? (j1 - j0 - w + 3) / 4 : j1 - j0);
+    // a wave's blocks: every SHARE-th from j0 + (its number) on
+    const int mine = j1 <= j0 ? 0 : (MERGE ? (j1 - j0 - w + SHARE - 1) / SHARE : j1 - j0);
     auto block_of = [&](int i) {
-        const int j = j0 + (MERGE ? w : 0) + i * step;
+        const int j = j0 + (MERGE ? w : 0) + i * SHARE;
         return j < ns ? j : j - ns + w0;
     };
     // (from the constant address space, for a scalar load: a vector load's wait would be one for
@@ -630,10 +631,10 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
     const size_t all = (size_t)s.T * a.q_heads;
     if constexpr (MERGE) {
         float(*const so)[16][LD] = reinterpret_cast<float(*)[16][LD]>(lds);
-        float(*const sm)[16] = reinterpret_cast<float(*)[16]>(lds + 4 * 16 * LD * 4), (*const sl)[16] = sm + 4;
+        float(*const sm)[16] = reinterpret_cast<float(*)[16]>(lds + WAVES * 16 * LD * 4), (*const sl)[16] = sm + WAVES;
         __syncthreads();                                   // (the waves' rings are done with)
         // what a thread adds up: four channels of a row
-        constexpr int TPR = D / 4, PASS = 256 / TPR;
+        constexpr int TPR = D / 4, PASS = 64 * WAVES / TPR;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
             if (n) __syncthreads();
@@ -648,11 +649,13 @@ __global__ __launch_bounds__(256, MERGE && D < 256 ? 3 : 2) void kv4_attend_kern
             __syncthreads();
             for (int r = threadIdx.x / TPR; r < 16 && row0 + 16 * n + r < rows; r += PASS) {
                 const int ch = threadIdx.x % TPR * 4;
-                const float mm = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
+                float mm = sm[0][r];
+#pragma unroll
+                for (int i = 1; i < WAVES; ++i) mm = fmaxf(mm, sm[i][r]);
                 float sum = 0.0f;
                 float4v acc = {0, 0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < WAVES; ++i) {
                     const float by = __builtin_amdgcn_exp2f(sm[i][r] - mm);
                     sum += by * sl[i][r];
                     acc += by * *reinterpret_cast<const float4v *>(&so[i][r][ch]);
@@ -780,22 +783,25 @@ template <int D, int NG>
 void launch_attend(const Kv4AttendPlan &p, const Kv4Cache &c, const Kv4Batch &s, const AttendArgs &a, hipStream_t st)
 {
     const dim3 grid((unsigned)p.workgroups);
-    if (p.shared)
-        hipLaunchKernelGGL((kv4_attend_kernel<D, NG, 1, true>), grid, dim3(256), 0, st, c, s, a);
+    if (p.shared == 8) {
+        if constexpr (D < 256)
+            hipLaunchKernelGGL((kv4_attend_kernel<D, NG, 1, 8>), grid, dim3(512), 0, st, c, s, a);
+    } else if (p.shared)
+        hipLaunchKernelGGL((kv4_attend_kernel<D, NG, 1, 4>), grid, dim3(256), 0, st, c, s, a);
     else
-        hipLaunchKernelGGL((kv4_attend_kernel<D, NG, D == 256 ? 1 : 2, false>), grid, dim3(256), 0, st, c, s, a);
+        hipLaunchKernelGGL((kv4_attend_kernel<D, NG, D == 256 ? 1 : 2, 1>), grid, dim3(256), 0, st, c, s, a);
 }
 
 } // namespace
 
-// Decode batches (up to 16 rows of a key/value head in a sequence): the four waves of
-// a workgroup share the rows.  More rows: each wave has 32 of its own (16 of 256 channels).
+// Decode batches (up to 16 rows of a key/value head in a sequence): the four or eight waves
+// of a workgroup share the rows.  More rows: each wave has 32 of its own (16 of 256 channels).
 Kv4AttendPlan kv4_attend_plan(int T, int max_new, int B, int q_heads, int heads, int D, int max_tokens, int window,
                               int sinks)
 {
     Kv4AttendPlan p;
     const long long R = q_heads / heads;
-    p.shared = max_new * R <= 16;
+    p.shared = max_new * R <= 16 ? 4 : 0;
     p.rows = p.shared || D == 256 ? 16 : 32;
     const int rb = p.shared ? p.rows : 4 * p.rows;
     // row blocks of all sequences: each has at most one that is not full.  (The grid holds
@@ -822,7 +828,12 @@ Kv4AttendPlan kv4_attend_plan(int T, int max_new, int B, int q_heads, int heads,
         // (joining them costs 5 us: not for fewer than two parts each of few tokens; 64 sequences
         // that see 1000 tokens each take 36 us in 96 parts, 29 whole.  Of many tokens a
         // sequence may be far longer than the others.)
-        if (n >= 2 * some || (n > some && tokens > 4096)) {
+        // Few tokens: eight waves are through with them before four and a second kernel are, where they
+        // have a CU each (one sequence of 8 heads: 500 tokens 8.1 us, 10.9 in parts; 1000 12.1 and
+        // 13.5, of it 12.0 on the GPU; 1500 15.2 and 12.1.  Four waves: 8.4, 13.4).
+        const bool eight = D < 256 && likely <= 256 && tokens <= 1024;
+        if (eight) p.shared = 8;
+        if (!eight && (n >= 2 * some || (n > some && tokens > 4096))) {
             p.items = (int)n;
             n = n - some + 1;
             p.splits = (int)(n < MAX_SPLITS ? n : MAX_SPLITS);

@@ -180,10 +180,10 @@ hipError_t launch_kv4_append(const Kv4Cache &c, const Kv4Batch &s, const void *k
                              const int32_t *positions, const float *cos_sin, int rot, int max_pos, bool inter,
                              void *q_out, hipStream_t st);
 hipError_t launch_kv4_read(const Kv4Cache &c, const Kv4Batch &s, int dtype, void *k_out, void *v_out, hipStream_t st);
-// How an attention call is cut: whether a workgroup's waves share their rows, rows of
+// How an attention call is cut: how many of a workgroup's waves share their rows, rows of
 // a wave, parts along the tokens, workgroups, bytes of workspace.
 struct Kv4AttendPlan {
-    bool shared;
+    int shared;                    // waves that share rows, 0: none
     int rows, splits, items;       // items (shared rows): parts of all rows of a key/value head
     long long workgroups;
     size_t bytes;
