@@ -830,8 +830,8 @@ Kv4AttendPlan kv4_attend_plan(int T, int max_new, int B, int q_heads, int heads,
         // sequence may be far longer than the others.)
         // Few tokens: eight waves are through with them before four and a second kernel are, where they
         // have a CU each (one sequence of 8 heads: 500 tokens 8.1 us, 10.9 in parts; 1000 12.1 and
-        // 13.5, of it 12.0 on the GPU; 1500 15.2 and 12.1.  Four waves: 8.4, 13.4).
-        const bool eight = D < 256 && likely <= 256 && tokens <= 1024;
+        // 13.5, of it 12.0 on the GPU; 1500 15.2 and 13.1.  Four waves: 8.4, 13.4).
+        const bool eight = D < 256 && likely <= 256 && tokens <= 1280;
         if (eight) p.shared = 8;
         if (!eight && (n >= 2 * some || (n > some && tokens > 4096))) {
             p.items = (int)n;

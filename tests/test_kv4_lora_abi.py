@@ -83,7 +83,9 @@ def _attend(q=FAKE, dtype=BF, T=4, ldq=1024, qh=8, new=2, off=FAKE, lens=FAKE, t
     (dict(ldq=1020), INV), (dict(ldq=1016), INV), (dict(qh=7), INV), (dict(qh=0), INV), (dict(new=0), INV),
     (dict(window=-1), INV), (dict(sinks=-1), INV), (dict(scale=0.0), INV), (dict(scale=-1.0), INV),
     (dict(scale=float("inf")), INV), (dict(scale=float("nan")), INV), (dict(flags=1), INV), (dict(dtype=F32), INV),
-    (dict(ws=None), WSP), (dict(nb=16), WSP), (dict(ws=P(0x10010)), INV),
+    # (four pages are seen without parts: no workspace is asked for)
+    (dict(ws=None), DEV), (dict(nb=16), DEV), (dict(ws=None, nb=0), DEV),
+    (dict(ws=None, width=64), WSP), (dict(nb=16, width=64), WSP), (dict(ws=P(0x10010), width=64), INV),
     (dict(T=2**24, qh=64, ldq=64 * 128), UNS),
 ])
 def test_attend_refusals(kw, rc):
