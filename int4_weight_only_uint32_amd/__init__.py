@@ -728,15 +728,16 @@ def _kv4_batch_args(T, seq_offsets, kv_lens, page_table, dev):
 def _kv4_rows(t: torch.Tensor, dtype, T, heads, D, dev, name):
     """The pointer of rows [T, heads, D], each row's heads together, and the elements from
     one row to the next."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (T, heads, D):
-        raise ValueError(f"{name} must be {[T, heads, D]}, got {list(t.shape)}")
-    if t.get_device() != dev:
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev >= 0 and t.dtype is dtype and
+            t.shape == (T, heads, D)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be a device tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != (T, heads, D):
+            raise ValueError(f"{name} must be {[T, heads, D]}, got {list(t.shape)}")
         raise ValueError(f"{name} is on {t.device}, not on GPU {dev}")
     ld, per_head, one = t.stride()
     if one != 1 or (heads > 1 and per_head != D):
