@@ -695,6 +695,9 @@ def kv4_cache(pages: int, heads: int, head_dim: int, page_size: int = 64, group:
     return KV4Cache(k=words(), v=words(), k_sz=sz(), v_sz=sz())
 
 
+_INT32, _FP16 = torch.int32, torch.float16
+
+
 def _kv4_cache_args(c: KV4Cache, dev):
     """The C entry points' arguments of a cache."""
     k, sz = c.k, c.k_sz
@@ -709,6 +712,14 @@ def _kv4_cache_args(c: KV4Cache, dev):
     if (pages | heads | page | d8) >> 28:
         _too_many(*shape)
     sz_shape = (pages, heads, groups, page, 2)
+    v, v_sz = c.v, c.v_sz
+    # (all checks of _arg at once: four calls less)
+    if (isinstance(v, torch.Tensor) and isinstance(v_sz, torch.Tensor) and
+            k.get_device() == v.get_device() == sz.get_device() == v_sz.get_device() == dev >= 0 and
+            k.dtype is v.dtype is _INT32 and sz.dtype is v_sz.dtype is _FP16 and
+            v.shape == shape and sz.shape == v_sz.shape == sz_shape and
+            k.is_contiguous() and v.is_contiguous() and sz.is_contiguous() and v_sz.is_contiguous()):
+        return (k.data_ptr(), v.data_ptr(), sz.data_ptr(), v_sz.data_ptr(), pages, heads, page, 8 * d8, 8 * d8 // groups)
     return (_arg(k, torch.int32, shape, dev, "cache.k"), _arg(c.v, torch.int32, shape, dev, "cache.v"),
             _arg(sz, torch.float16, sz_shape, dev, "cache.k_sz"),
             _arg(c.v_sz, torch.float16, sz_shape, dev, "cache.v_sz"), pages, heads, page, 8 * d8, 8 * d8 // groups)
@@ -721,6 +732,11 @@ def _kv4_batch_args(T, seq_offsets, kv_lens, page_table, dev):
     B, width = page_table.shape
     if (T | B | width) >> 31:
         _too_many(T, B, width)
+    if (isinstance(kv_lens, torch.Tensor) and kv_lens.get_device() == page_table.get_device() == dev >= 0 and
+            kv_lens.dtype is page_table.dtype is _INT32 and kv_lens.shape == (B,) and kv_lens.is_contiguous() and
+            page_table.is_contiguous()):
+        return (_arg(seq_offsets, _INT32, (B + 1,), dev, "seq_offsets"), kv_lens.data_ptr(), page_table.data_ptr(), B,
+                width)
     return (_arg(seq_offsets, torch.int32, (B + 1,), dev, "seq_offsets"), _arg(kv_lens, torch.int32, (B,), dev, "kv_lens"),
             _arg(page_table, torch.int32, (B, width), dev, "page_table"), B, width)
 
