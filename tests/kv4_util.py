@@ -107,8 +107,8 @@ def attend(q, cache, lens, off, table, scale, window=0, sinks=0):
       * p_t in 32 bits: the score's sum of D products (2^-24 of their sizes for each of
         the D/32 + 8 additions in a row), its product with the scale, and 2^-22 for
         the exponential; the same for their sum;
-      * the sum of a group's queries as two 16-bit values, 2^-25 of 2^-9 of a power of two
-        over the row's largest query and up to twice that: 2^-16 times 2 max |q| times |z|;
+      * the sum of a group's queries as two 16-bit values, and codes that enter as 64 + code: within
+        2^-16 times 2 max |q| times |z| for each group (zeros are 7.5 scales and more here);
       * products and sums in 32 bits, 2^-20 of their sizes.
     """
     kd, vd = values_of(cache)

@@ -366,3 +366,49 @@ def test_pages_past_32_bits():
     a = qg.kv4_read(cache, lens.cuda(), table.cuda(), seq_offsets=off.cuda(), rows=600)
     b = qg.kv4_read(to_gpu(small), lens.cuda(), moved.cuda(), seq_offsets=off.cuda(), rows=600)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("H,R,D,g,dtype", [(2, 3, 64, 64, "bf16"), (1, 8, 128, 32, "fp16")])
+def test_attend_parts_of_many_ragged_sequences(H, R, D, g, dtype):
+    """More sequences than lanes, one far longer than the others, some empty: parts of one size."""
+    rnd, gen = rng(11)
+    lens = [rnd.choice((0, 1, 5, 33, 64, 70)) for _ in range(100)]
+    lens[70], lens[3] = 5000, 900
+    note(f"attend parts H={H} R={R} D={D} g={g} {dtype}")
+    lens_t, off, table, pages = batch(rnd, lens, [1] * 100, 64)
+    c = random_cache(gen, pages, H, D, 64, g)
+    q = _rows(gen, 100, H * R, D, HALF[dtype])
+    out = _check(q, c, lens_t, off, table, max_new=1)
+    for _ in range(3):
+        again = qg.kv4_attend(q.cuda(), to_gpu(c), lens_t.cuda(), table.cuda())
+        assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("D,g,R,lens,news", [(128, 64, 5, [1500, 300], [1, 1]), (128, 32, 4, [300], [100]),
+                                             (64, 64, 8, [2500], [1]), (256, 32, 2, [400], [1])])
+def test_attend_scales_of_all_sizes(D, g, R, lens, news):
+    """Scales from 1e-4 to 3000 and constant groups, the large ones late: the reference of p moves."""
+    rnd, gen = rng(12 + D + g)
+    note(f"attend scales D={D} g={g} R={R} lens={lens} news={news}")
+    lens_t, off, table, pages = batch(rnd, lens, news, 64)
+    c = random_cache(gen, pages, 1, D, 64, g)
+    for b, n in enumerate(lens):
+        for i in range(-(-n // 64)):
+            p = int(table[b, i])
+            size = (1e-4, 0.02, 1.0, 0.0, 40.0, 3000.0)[min(5, 6 * i * 64 // n)]
+            s = (size * (0.5 + 0.5 * torch.rand(c.v_sz[p, ..., 0].shape, generator=gen))).half()
+            c.v_sz[p, ..., 0], c.v_sz[p, ..., 1] = s, (-7.5 * s.float()).half()
+    q = _rows(gen, int(off[-1]), R, D, torch.float16)
+    _check(q, c, lens_t, off, table, max_new=max(news))
+    _check(q, c, lens_t, off, table, max_new=max(news), window=200, sinks=3)
+
+
+@pytest.mark.parametrize("D,g", [(64, 64), (128, 128), (256, 128)])
+def test_attend_largest_query_sums(D, g):
+    """Queries whose channels are all the largest of a power of two: 64 times their sum is the largest binary16."""
+    rnd, gen = rng(13 + D)
+    lens_t, off, table, pages = batch(rnd, [100], [1], 64)
+    c = random_cache(gen, pages, 1, D, 64, g)
+    q = torch.full((1, 2, D), 2047 / 2048, dtype=torch.float16)
+    q[:, 1] = -q[:, 1]
+    _check(q, c, lens_t, off, table, max_new=1, scale=1e-3)
