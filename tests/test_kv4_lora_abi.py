@@ -44,6 +44,7 @@ def _append(k=FAKE, v=FAKE, q=None, dtype=BF, T=4, ldk=256, ldv=256, ldq=1024, q
     (dict(k=None), INV), (dict(v=None), INV), (dict(k=P(0x10008)), INV), (dict(ldk=250), INV), (dict(ldk=248), INV),
     (dict(ldv=0), INV), (dict(ldv=-256), INV), (dict(q=FAKE), INV), (dict(q=FAKE, qo=P(0x10008)), INV),
     (dict(q=FAKE, qo=FAKE, ldq=1016), INV), (dict(q=FAKE, qo=FAKE, qh=0), INV), (dict(q=FAKE, qo=FAKE, qh=2**19), INV),
+    (dict(q=FAKE, qo=FAKE, qh=2**18, ldq=2**25), INV),
     (dict(rot=144), UNS), (dict(rot=-16), UNS), (dict(rot=24), UNS), (dict(cs=None), INV), (dict(maxp=0), INV),
     (dict(cs=P(0x10004)), INV), (dict(pos=P(0x10002)), INV), (dict(flags=2), INV), (dict(dtype=F32), INV),
     (dict(T=2**28), UNS),
@@ -87,6 +88,8 @@ def _attend(q=FAKE, dtype=BF, T=4, ldq=1024, qh=8, new=2, off=FAKE, lens=FAKE, t
     (dict(ws=None), DEV), (dict(nb=16), DEV), (dict(ws=None, nb=0), DEV),
     (dict(ws=None, width=64), WSP), (dict(nb=16, width=64), WSP), (dict(ws=P(0x10010), width=64), INV),
     (dict(T=2**24, qh=64, ldq=64 * 128), UNS),
+    # a launch's threads: 2^17 blocks of rows of 64 heads, 512 threads each where few tokens are seen
+    (dict(T=2**21, H=64, qh=64, ldq=64 * 128, new=1), UNS), (dict(T=2**20, H=64, qh=64, ldq=64 * 128, new=1), DEV),
 ])
 def test_attend_refusals(kw, rc):
     assert _attend(**kw) == rc
@@ -101,6 +104,7 @@ def test_attend_workspace_sizes():
     assert n > 8 * 130 * 4 and n % (8 * 4) == 0                   # parts of 8 rows of 128 values, maximum and sum; their number
     assert f(1, 1, 1, 8, 8, 128, 2048, 64, 128, 0) < n            # a window needs fewer
     assert f(4096, 4096, 1, 64, 8, 128, 2048, 64, 0, 0) == 0      # enough rows: no parts
+    assert f(2**24, 1, 1, 8, 8, 128, 2048, 64, 0, 0) == 0         # nor where max_new says there are few
     for args in ((-1, 1, 1, 8, 8, 128, 4, 64, 0, 0), (1, 0, 1, 8, 8, 128, 4, 64, 0, 0), (1, 1, 1, 8, 3, 128, 4, 64, 0, 0),
                  (1, 1, 1, 8, 8, 128, 0, 64, 0, 0), (1, 1, 1, 8, 8, 128, 2**25, 64, 0, 0), (1, 1, 1, 8, 8, 128, 4, 64, -1, 0)):
         assert f(*args) == bad and qg.lib().qg_last_error()
