@@ -458,15 +458,15 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
                     za[t][r] = !some || odd_word(za[t][r]) ? 0u : za[t][r];
                 }
         }
-        // the largest of the scales, over all groups and tokens in one lane or another
-        typedef unsigned short ushort2v __attribute__((ext_vector_type(2)));
-        ushort2v large = __builtin_bit_cast(ushort2v, za[0][0]);
+        // the largest of the scales, over all groups and tokens in one lane or another.  (A word's lower half
+        // by conversion: a bit cast of a vector's element takes the vector's first one.)
+        unsigned short large = (unsigned short)za[0][0];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) large = __builtin_elementwise_max(large, __builtin_bit_cast(ushort2v, za[i / 4][i % 4]));
-        bool raise = room > -3 && large.x > (unsigned)(28 - room) << 10;
+        for (int i = 1; i < 8; ++i) large = __builtin_elementwise_max(large, (unsigned short)za[i / 4][i % 4]);
+        bool raise = room > -3 && large > (unsigned)(28 - room) << 10;
         float less = 0.0f;
         if (__any(raise)) {
-            int e = large.x >> 10;                         // vs < 2^(e - 14)
+            int e = large >> 10;                           // vs < 2^(e - 14)
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
                 const int other = __shfl_xor(e, o);
