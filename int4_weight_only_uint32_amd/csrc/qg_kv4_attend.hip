@@ -428,8 +428,23 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
             za[t] = vsz[zg * 8 + t * 4];
         }
         __builtin_amdgcn_sched_barrier(0);
-        // all rows see all of the block, or some do not: a bit for each score that is hidden
-        const bool whole = ASK_FIRST ? asked : sees_all(t0, ok);
+        // the largest of the values' scales, over all groups and tokens in one lane or another.  (A word's
+        // lower half by conversion: a bit cast of a vector's element takes the vector's first one.)
+        const auto largest = [&] {
+            unsigned short v = (unsigned short)za[0][0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) v = __builtin_elementwise_max(v, (unsigned short)za[i / 4][i % 4]);
+            return v;
+        };
+        // all rows see all of the block, or some do not: a bit for each score that is hidden.  (A
+        // scale that is no number goes that way, too: here it would meet the zeros of the products with
+        // ones, and spoil the other groups' sums.)
+        bool whole = ASK_FIRST ? asked : sees_all(t0, ok);
+        unsigned short large = 0;
+        if (!ASK_FIRST && whole) {
+            large = largest();
+            whole = !__any(large >= 0x7C00);
+        }
         unsigned hide[NQ];
         if (!whole) {
 #pragma unroll
@@ -447,8 +462,8 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
             }
         }
         if (!whole) {
-            // a token that one row sees and another does not must not bring it a NaN: 0 here, and a NaN
-            // put in where it is seen; one that no row sees counts for nothing
+            // a token that one row sees and another does not must not bring it a NaN, nor one group the
+            // others: 0 here, and a NaN put in where it is seen; one that no row sees counts for nothing
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -458,11 +473,7 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
                     za[t][r] = !some || odd_word(za[t][r]) ? 0u : za[t][r];
                 }
         }
-        // the largest of the scales, over all groups and tokens in one lane or another.  (A word's lower half
-        // by conversion: a bit cast of a vector's element takes the vector's first one.)
-        unsigned short large = (unsigned short)za[0][0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) large = __builtin_elementwise_max(large, (unsigned short)za[i / 4][i % 4]);
+        if (ASK_FIRST || !whole) large = largest();
         bool raise = room > -3 && large > (unsigned)(28 - room) << 10;
         float less = 0.0f;
         if (__any(raise)) {
@@ -610,7 +621,16 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
         }
         const int t0 = block_of(i) << 5;
         const bool ok = (has & 1u) != 0;
-        block(ASK_FIRST && sees_all(t0, ok), ring + (i % RG::STAGES) * RG::BYTES, t0, ok);
+        const uint8_t *const x = ring + (i % RG::STAGES) * RG::BYTES;
+        bool asked = false;
+        if (ASK_FIRST) {
+            const unsigned *const scales = reinterpret_cast<const unsigned *>(x + 2 * RG::CODES) + 32 * NG;
+            bool odd = false;
+#pragma unroll
+            for (int u = 0; u < NG / 2; ++u) odd |= (scales[64 * u + lane] & 0x7C00u) == 0x7C00u;
+            asked = sees_all(t0, ok) && !__any(odd);
+        }
+        block(asked, x, t0, ok);
         has >>= 1;
     }
 
