@@ -777,8 +777,9 @@ __global__ __launch_bounds__(512) void kv4_join_kernel(Kv4Batch s, AttendArgs a)
     m = fmaxf(top[0], top[1]);
     if (tid < MAX_SPLITS) {
         const float e = __builtin_amdgcn_exp2f(mi - m);
-        // a part without a token has no values to be read
-        by[tid] = li == 0.0f ? 0.0f : e;
+        // a part without a token has no values to be read: -1.  (Others are added also where their weight
+        // is 0: they may be no numbers.)
+        by[tid] = li == 0.0f ? -1.0f : e;
         li = li == 0.0f ? 0.0f : li * e;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) li += __shfl_xor(li, o);
@@ -790,8 +791,8 @@ __global__ __launch_bounds__(512) void kv4_join_kernel(Kv4Batch s, AttendArgs a)
 #pragma unroll
     for (int i = 0; i < MOST; ++i) {
         const int k = grp + i * GR;
-        const float e = k < MAX_SPLITS ? by[k] : 0.0f;
-        if (e != 0.0f) acc += e * v[i];
+        const float e = k < MAX_SPLITS ? by[k] : -1.0f;
+        if (!(e < 0.0f)) acc += e * v[i];
     }
     so[grp][tid % TPR] = acc;
     debug_stage_sync();

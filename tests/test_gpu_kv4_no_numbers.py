@@ -85,3 +85,24 @@ def test_appended_values_past_fp16():
                             max_new=hint).cpu()
         nan = torch.isnan(out)
         assert bool(nan[0, 3:, 64:].all()) and int(nan.sum()) == 3 * 64
+
+
+@pytest.mark.parametrize("D,g,n", [(128, 64, 6000), (64, 64, 2500), (256, 32, 2500), (128, 64, 700)])
+def test_a_weight_of_nothing_does_not_hide_it(D, g, n):
+    """A seen group is no number however small its weight is: here 2^-400 and less of another
+    part's, beside which it comes to 0 in 32 bits."""
+    rnd, gen = rng(D + n)
+    lens, off, table, pages = batch(rnd, [n], [1], 64)
+    c = random_cache(gen, pages, 1, D, 64, g, spread=0.01)
+    p, t = int(table[0, (n - 10) // 64]), (n - 10) % 64
+    c.k_sz[p, 0, :, t] = torch.tensor([0.0, 8.0]).half()
+    q = torch.ones((1, 2, D), dtype=torch.float16)
+    ref, tol = attend(q, c, lens, off, table, 0.6)
+    bad = qg.KV4Cache(c.k, c.v, c.k_sz, c.v_sz.clone())
+    bad.v_sz[int(table[0, 0]), 0, 0, 5] = math.nan
+    for hint in (1, 100):
+        note(f"no weight D={D} g={g} n={n} max_new={hint}")
+        clean = _run(q, c, lens, off, table, hint, scale=0.6).cpu()
+        assert bool(((clean.double() - ref).abs() <= tol).all())
+        out = _run(q, bad, lens, off, table, hint, scale=0.6).cpu()
+        assert bool(torch.isnan(out[..., :g]).all()) and torch.equal(out[..., g:], clean[..., g:])
