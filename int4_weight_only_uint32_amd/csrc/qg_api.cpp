@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -906,7 +907,7 @@ int kv4_attend(const void *q, int dtype, int T, int ld_q, int q_heads, int max_n
     if (rc) return rc;
     if ((rc = check_dtype16(what, dtype))) return rc;
     if ((rc = check_attend_shape(what, T, max_new, B, q_heads, heads, window, sinks))) return rc;
-    if (!(scale > 0.0f) || scale > 3.0e38f) return fail(QG_ERR_INVALID_ARG, "%s: scale must be finite and > 0", what);
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(QG_ERR_INVALID_ARG, "%s: scale must be finite and > 0", what);
     if (flags != 0) return fail(QG_ERR_INVALID_ARG, "%s: unknown flags 0x%x", what, flags);
     if (T == 0 || B == 0) return ok();
     if ((rc = check_kv4_rows(what, "q", q, ld_q, q_heads, head_dim))) return rc;

@@ -17,6 +17,8 @@
 // the columns of its products and the tokens as the rows: a lane then holds the scores of
 // one query row against four consecutive tokens of each of two 16-token tiles, which
 // is what the second product takes from it.
+#include <cmath>
+
 #include "qg_kv4.h"
 #include "qg_launch.h"
 
@@ -29,7 +31,8 @@ struct AttendArgs {
     long long ldq;
     int q_heads, R;                // R: query heads of one key/value head
     bool bf16;
-    float scale;                   // softmax scale times log2 e
+    float scale;                   // softmax scale times log2 e, as scale 2^scale_ex
+    int scale_ex;
     int window, sinks;             // window 0: none
     int splits, items;             // most parts of a row's blocks; items of all sequences (SHARED)
     float *part, *ml;              // splits > 1: [splits][T * q_heads][D], and [..][2] maxima and sums
@@ -290,7 +293,7 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
         bad |= __shfl_xor((int)bad, 32) != 0;
         int ex = 0;
         if (big > 0.0f && !bad) (void)frexpf(big, &ex);    // big < 2^ex
-        f[n] = bad ? __builtin_nanf("") : ldexpf(a.scale, ex - 3);
+        f[n] = bad ? __builtin_nanf("") : ldexpf(a.scale, a.scale_ex + ex - 3);
         float qs[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -890,8 +893,10 @@ hipError_t launch_kv4_attend(const Kv4AttendPlan &p, const Kv4Cache &c, const Kv
 {
     const size_t all = (size_t)s.T * q_heads;
     float *const part = (float *)ws;
+    int scale_ex;
+    const float log2_scale = frexpf(scale, &scale_ex) * 1.4426950408889634f;
     const AttendArgs a = {(const uint16_t *)q, (uint16_t *)out, ldq, q_heads, q_heads / c.heads, dtype == QG_DT_BF16,
-                          scale * 1.4426950408889634f, window, sinks, p.splits, p.items, part,
+                          log2_scale, scale_ex, window, sinks, p.splits, p.items, part,
                           part ? part + (size_t)p.splits * all * c.D : nullptr,
                           part ? (int32_t *)(part + (size_t)p.splits * all * (c.D + 2)) : nullptr};
     const int ng = c.D / c.g;
