@@ -854,7 +854,7 @@ def kv4_attend(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, page_tab
     """Causal attention of the sequences' last tokens (q [T, q_heads, head_dim], one row a sequence
     or seq_offsets' ragged runs) over the cache that holds them; window > 0: each token
     sees that many, itself among them, and the first `sinks`.  max_new: the expected largest
-    number of rows of a sequence (default: T with seq_offsets)."""
+    number of rows of a sequence (default with seq_offsets: their mean, rounded up)."""
     d = _dtype(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [T, q_heads, head_dim]")
@@ -865,7 +865,7 @@ def kv4_attend(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, page_tab
     batch = _kv4_batch_args(T, seq_offsets, kv_lens, page_table, dev)
     qp, ldq = _kv4_rows(q, q.dtype, T, q_heads, D, dev, "q")
     if max_new is None:
-        max_new = 1 if seq_offsets is None else max(T, 1)
+        max_new = 1 if seq_offsets is None else max(-(-T // max(batch[3], 1)), 1)
     for n in (max_new, window, sinks):
         if not 0 <= n < 1 << 31:
             raise ValueError(f"max_new, window and sinks {(max_new, window, sinks)} must lie in 0 .. 2^31 - 1")
