@@ -3,10 +3,10 @@
 // A token's row of D channels of one head is D/g groups of g channels; each holds
 // 4-bit codes, an fp16 scale s and an fp16 zero z, and stands for code * s + z.
 //
-// Codes are laid out as operands of the 16x16x32 fp16 MFMA, split without a
-// multiplication: a nibble ANDed out of a word is the binary16 subnormal
-// v * 2^-24 (low nibbles) or 16 v * 2^-24 (high ones), both exact inputs, and the
-// factor 16 goes into the other operand.
+// Codes are laid out as operands of the 16x16x32 fp16 MFMA, made without a
+// multiplication or an exchange between lanes: two nibbles of a word, shifted to bits 4 to 7 of
+// its halves and ORed with the exponent of 64, are the binary16 values 64 + code, and
+// 64 times the sum of the other operand is taken off the product again.
 //   keys    a token's D/8 words are [4][D/32]: lane group q of the MFMA owns words
 //           (q, 0 .. D/32 - 1).  Nibble 4a + 2b + c of word (q, 2i + l) is channel
 //           32 (i + c D/64) + 8 q + 4 l + 2 b + a: words 2i, 2i + 1 hold the eight

@@ -85,12 +85,12 @@ __device__ inline void wait_loads()
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// A wave's ring of 32-token blocks in LDS.  Loads go there directly: keys and values
+// A wave's ring of two 32-token blocks in LDS.  Loads go there directly: keys and values
 // as they lie, then scales and zeros, [keys | values][group][32] words (repeated up
 // to whole loads of 64 lanes).
-template <int D, int NG, int DEPTH>
+template <int D, int NG>
 struct Ring {
-    static constexpr int STAGES = DEPTH;
+    static constexpr int STAGES = 2;
     static constexpr int CODES = 32 * D / 2;                       // bytes of a block's keys, or of its values
     static constexpr int SCALES = NG > 4 ? 256 * NG : 1024;
     static constexpr int BYTES = 2 * CODES + SCALES;
@@ -134,7 +134,8 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
     constexpr bool MERGE = SHARE > 1;
     constexpr int WAVES = MERGE ? SHARE : 4;
     constexpr int ROWS = 16 * NQ, RB = MERGE ? ROWS : 4 * ROWS;
-    using RG = Ring<D, NG, 2>;
+    using RG = Ring<D, NG>;
+    static_assert(!MERGE || NQ == 1, "waves that share rows have 16");
     constexpr int LD = D + 4;                              // (a row of the waves' results)
     constexpr int RINGS = WAVES * RG::STAGES * RG::BYTES, SUMS = MERGE ? WAVES * 16 * (LD + 2) * 4 : 0;
     // (one array for all: with several the compiler puts a wait for all loads before each
@@ -249,21 +250,14 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
         for (int u = 0; u < SLOADS; ++u) lds_load16<MERGE ? QG_NT : 0>(sz0[u] + sat, to + 2 * RG::CODES + u * 1024);
     };
 
-    // the first blocks; a bit for each in flight says whether it has a page
-    constexpr int AHEAD = RG::STAGES - 1;
-    unsigned has = 0;
+    // the first block, and the second one's page; whether a block has a page
+    bool has = false;
     int next = 0;                                          // the page of the block to be asked for next
     if (mine > 0) {
-        int pg[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) pg[i] = page_of(i < mine ? i : 0);
-        next = page_of(AHEAD < mine ? AHEAD : 0);
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-            if (i < mine) {
-                has |= ((unsigned)pg[i] < (unsigned)c.pages ? 1u : 0u) << i;
-                load(i, pg[i]);
-            }
+        const int pg = page_of(0);
+        next = page_of(mine > 1 ? 1 : 0);
+        has = (unsigned)pg < (unsigned)c.pages;
+        load(0, pg);
     }
 
     // the queries as operands, q' = q 2^(3 - ex) below 8 (64 times their sum is a binary16
@@ -607,23 +601,19 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
 
     for (int i = 0; i < mine; ++i) {
         const int more = mine - 1 - i;                     // blocks behind this one
-        if (more >= AHEAD) {
-            has |= ((unsigned)next < (unsigned)c.pages ? 1u : 0u) << AHEAD;
+        const bool ok = has;
+        if (more > 0) {
+            has = (unsigned)next < (unsigned)c.pages;
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage's last reads are done
-            load(i + AHEAD, next);
+            load(i + 1, next);
             debug_stage_sync();
-            wait_loads<AHEAD * RG::LOADS>();
-            __builtin_amdgcn_sched_barrier(0);             // (behind that wait, or it waits for this load)
-            next = page_of(more > AHEAD ? i + AHEAD + 1 : i);
-        } else if (AHEAD > 2 && more == 2) {
-            wait_loads<2 * RG::LOADS>();
-        } else if (AHEAD > 1 && more == 1) {
             wait_loads<RG::LOADS>();
+            __builtin_amdgcn_sched_barrier(0);             // (behind that wait, or it waits for this load)
+            next = page_of(more > 1 ? i + 2 : i);
         } else {
             wait_loads<0>();
         }
         const int t0 = block_of(i) << 5;
-        const bool ok = (has & 1u) != 0;
         const uint8_t *const x = ring + (i % RG::STAGES) * RG::BYTES;
         bool asked = false;
         if (ASK_FIRST) {
@@ -634,7 +624,6 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
             asked = sees_all(t0, ok) && !__any(odd);
         }
         block(asked, x, t0, ok);
-        has >>= 1;
     }
 
     // a column's sum of p, and its values with the zeros' part, from the lane groups that hold them
@@ -666,49 +655,45 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
         // what a thread adds up: four channels of a row
         constexpr int TPR = D / 4, PASS = 64 * WAVES / TPR;
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-            if (n) __syncthreads();
+        for (int d = 0; d < DT; ++d)
+            *reinterpret_cast<float4v *>(&so[w][col][16 * d + 4 * kq]) = o[0][d];
+        if (kq == 0) {
+            sm[w][col] = m[0];
+            sl[w][col] = l[0];
+        }
+        debug_stage_sync();
+        __syncthreads();
+        for (int r = threadIdx.x / TPR; r < 16 && row0 + r < rows; r += PASS) {
+            const int ch = threadIdx.x % TPR * 4;
+            float mm = sm[0][r];
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
-                *reinterpret_cast<float4v *>(&so[w][col][16 * d + 4 * kq]) = o[n][d];
-            if (kq == 0) {
-                sm[w][col] = m[n];
-                sl[w][col] = l[n];
+            for (int i = 1; i < WAVES; ++i) mm = fmaxf(mm, sm[i][r]);
+            float sum = 0.0f;
+            float4v acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < WAVES; ++i) {
+                const float by = __builtin_amdgcn_exp2f(sm[i][r] - mm);
+                sum += by * sl[i][r];
+                acc += by * *reinterpret_cast<const float4v *>(&so[i][r][ch]);
             }
-            debug_stage_sync();
-            __syncthreads();
-            for (int r = threadIdx.x / TPR; r < 16 && row0 + 16 * n + r < rows; r += PASS) {
-                const int ch = threadIdx.x % TPR * 4;
-                float mm = sm[0][r];
-#pragma unroll
-                for (int i = 1; i < WAVES; ++i) mm = fmaxf(mm, sm[i][r]);
-                float sum = 0.0f;
-                float4v acc = {0, 0, 0, 0};
-#pragma unroll
-                for (int i = 0; i < WAVES; ++i) {
-                    const float by = __builtin_amdgcn_exp2f(sm[i][r] - mm);
-                    sum += by * sl[i][r];
-                    acc += by * *reinterpret_cast<const float4v *>(&so[i][r][ch]);
+            const int rr = row0 + r, i = rr / R;
+            const size_t g = ((size_t)seq.row + i) * a.q_heads + (size_t)h * R + (rr - i * R);
+            if (a.splits > 1) {
+                if (ch == 0 && split == 0) a.parts[g] = per < nb ? (nb + per - 1) / per : 1;
+                if (ch == 0) {
+                    a.ml[(split * all + g) * 2] = mm;
+                    a.ml[(split * all + g) * 2 + 1] = sum;
                 }
-                const int rr = row0 + 16 * n + r, i = rr / R;
-                const size_t g = ((size_t)seq.row + i) * a.q_heads + (size_t)h * R + (rr - i * R);
-                if (a.splits > 1) {
-                    if (ch == 0 && split == 0) a.parts[g] = per < nb ? (nb + per - 1) / per : 1;
-                    if (ch == 0) {
-                        a.ml[(split * all + g) * 2] = mm;
-                        a.ml[(split * all + g) * 2 + 1] = sum;
-                    }
-                    if (j0 < j1) *reinterpret_cast<float4v *>(a.part + (split * all + g) * D + ch) = acc;
-                } else {
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    uint2v r2;
-                    uint16_t v[4];
+                if (j0 < j1) *reinterpret_cast<float4v *>(a.part + (split * all + g) * D + ch) = acc;
+            } else {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                uint2v r2;
+                uint16_t v[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = a.bf16 ? f2bf(acc[e] * inv) : f2h(acc[e] * inv);
-                    r2.x = v[0] | (uint32_t)v[1] << 16;
-                    r2.y = v[2] | (uint32_t)v[3] << 16;
-                    *reinterpret_cast<uint2v *>(a.out + g * D + ch) = r2;
-                }
+                for (int e = 0; e < 4; ++e) v[e] = a.bf16 ? f2bf(acc[e] * inv) : f2h(acc[e] * inv);
+                r2.x = v[0] | (uint32_t)v[1] << 16;
+                r2.y = v[2] | (uint32_t)v[3] << 16;
+                *reinterpret_cast<uint2v *>(a.out + g * D + ch) = r2;
             }
         }
     } else {
