@@ -485,7 +485,8 @@ int moe_combine_rows(const void *Y, int dtype, const int32_t *slot_row, const fl
  *            z = fp16(min x),  s = fp16((max x - min x) / 15),
  *            c = clamp(round_half_even((x - z) / s), 0, 15),  0 where s is 0.
  *          A group with a NaN or with values past fp16's range gets NaN scale
- *          and zero and codes 0, and so is NaN wherever it is seen.
+ *          and zero and codes 0, and so is NaN wherever it is seen: one of
+ *          values in its own channels, one of keys in the rows that see it.
  * No two rows of a call may name the same place of the cache.  One kernel, no
  * workspace.                                                                */
 #define QG_KV4_INTERLEAVED 0x1u
@@ -516,7 +517,14 @@ int kv4_read(const uint32_t *cache_k, const uint32_t *cache_v, const uint16_t *c
  *          stay visible).  A row that sees nothing gets zeros.
  * scale    finite and > 0.
  * max_new  the expected largest number of rows of a sequence: it only picks the
- *          kernel, so a wrong one is slower, never wrong.
+ *          kernel, for all of a call's sequences.  Up to 16 rows of a key/value head
+ *          (max_new * q_heads / heads) the waves of a workgroup share a sequence's tokens,
+ *          and these are cut into parts; above, each wave walks all tokens of its own 32 rows
+ *          (16 of 256 channels), in parts only where there are few rows.  So single tokens
+ *          with long contexts are far slower beside a long run than in a call of
+ *          their own: give them one.
+ * max_pages, the table's width, also sizes the launch: a table far wider than the
+ *          sequences need costs up to a third more time.
  * Scores, the softmax's maximum and sum and the accumulators are fp32; the
  * codes enter the products exactly, and so do a query's channels down to
  * 2^-17 of its largest (smaller ones within 2^-28 of that); p_t, against zeros

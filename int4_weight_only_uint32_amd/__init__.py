@@ -813,7 +813,7 @@ def kv4_read(cache: KV4Cache, kv_lens: torch.Tensor, page_table: torch.Tensor,
              v_out: Optional[torch.Tensor] = None, rows: Optional[int] = None, dtype: torch.dtype = torch.bfloat16):
     """The last rows of each sequence (as many as seq_offsets gives each, one without it) back from the cache as
     values: (keys, values) [T, heads, head_dim].  `rows` is T where seq_offsets is given and
-    k_out is not."""
+    k_out is not.  Rows of no sequence are not written (of new tensors: not initialized)."""
     dev = page_table.get_device()
     cargs = _kv4_cache_args(cache, dev)
     heads, D = cargs[5], cargs[7]
@@ -854,7 +854,10 @@ def kv4_attend(q: torch.Tensor, cache: KV4Cache, kv_lens: torch.Tensor, page_tab
     """Causal attention of the sequences' last tokens (q [T, q_heads, head_dim], one row a sequence
     or seq_offsets' ragged runs) over the cache that holds them; window > 0: each token
     sees that many, itself among them, and the first `sinks`.  max_new: the expected largest
-    number of rows of a sequence (default with seq_offsets: their mean, rounded up)."""
+    number of rows of a sequence (default with seq_offsets: their mean, rounded up); it picks one
+    kernel for the whole call, so single tokens with long contexts belong in another call than
+    long runs (see include/qgemm.h).  Rows of no sequence are not written (of a new tensor: not
+    initialized)."""
     d = _dtype(q, "q")
     if q.dim() != 3:
         raise ValueError("q must be [T, q_heads, head_dim]")

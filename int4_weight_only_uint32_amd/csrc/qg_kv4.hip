@@ -207,8 +207,9 @@ __global__ __launch_bounds__(THREADS, D < 256 ? 6 : 4) void kv4_append_kernel(Kv
         bad |= (zb & 0x7C00) == 0x7C00 || (f2h(mx) & 0x7C00) == 0x7C00;
         const uint16_t sb = bad ? 0x7E00 : f2h((mx - mn) / 15.0f);
         const float sc = h2f(sb), z = h2f(zb);
-        // (x - z) / s to the nearest whole number: by the reciprocal, whose product is within 2^-19
-        // of a quotient up to 16, and by the division where that lies near the middle of two
+        // (x - z) / s to the nearest whole number: by the reciprocal, whose product is within 2^-17
+        // of a quotient up to 16 (16 times two steps, 2^-22, and a rounding, 2^-24), and by the
+        // division where that lies within 2^-16 of the middle of two
         const float rs = sc > 0.0f ? rcp_wide(sc) : 0.0f;
         float q[8], near = 0.0f;
 #pragma unroll

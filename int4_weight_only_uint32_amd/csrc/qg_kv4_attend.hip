@@ -120,13 +120,16 @@ __device__ inline SeenBlocks seen_blocks(int p0, int p1, int window, int sinks, 
 
 // SHARE 4 or 8: the workgroup's waves, as many, share 16 NQ rows and take every SHARE-th block
 // of tokens; their results meet in LDS at the end.  SHARE 1: each of four has rows of its own.
-// Bound by the issue of VALU instructions (about 330 a block and wave with 16 rows and as many with
-// 32, a third of them codes that become operands), so 32 rows where there are as many, and three
-// waves a SIMD (two with 32 rows) rather than longer rings: with four stages and two waves 16
-// sequences of up to 8191 take 38 us, 32 so.  Measured with heads of 128, 8 of keys and values:
-// these 16, 40 query heads, 32 us with their joining (114 MB, 3.6 TB/s); one sequence of 131072, 64
-// heads, 35 with it (143 MB, 4.1 TB/s); two prompts' 2048 rows, 40 heads, against 6100 tokens 490 us
-// (542 TFLOP/s, products 28 % of the time).
+// A block and wave are about 335 VALU instructions with two groups (295 with one, 451 with four),
+// with 16 rows as with 32, a third of them codes that become operands; so 32 rows where there are
+// as many, and three waves a SIMD (two with 32 rows) rather than longer rings: with four stages and
+// two waves 16 sequences of up to 8191 take 38 us, 32 so.  Prompts are bound by that issue (69 % of the SIMDs' cycles) and the products (27 %),
+// which hardly overlap with two waves; single tokens by no one thing: VALU issue is 49 to 59 % of
+// the cycles, products 9 to 14 %, and a wave waits at a wait or barrier for 31 to 43 % of its time
+// (the start's dependent loads, a ring of two blocks, the waves' and the parts' uneven ends).
+// Measured with heads of 128, 8 of keys and values: these 16, 40 query heads, 32 us with their
+// joining (114 MB, 3.6 TB/s); one sequence of 131072, 64 heads, 35 to 36 with it (143 MB, 4.0 TB/s);
+// two prompts' 2048 rows, 40 heads, against 6100 tokens 500 to 505 us (528 TFLOP/s).
 template <int D, int NG, int NQ, int SHARE>
 __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 : 2) void kv4_attend_kernel(Kv4Cache c, Kv4Batch s, AttendArgs a)
 {
@@ -348,7 +351,8 @@ __global__ __launch_bounds__(SHARE == 8 ? 512 : 256, SHARE == 4 && D < 256 ? 3 :
     // keeps 214 of them instead of 256 and 18 in memory with four groups of 32 rows, and interleaves less.
     // 2 x 1024 rows of 32 heads against 4096 tokens, groups of 32 of 128 channels: 348 us, 370 the other
     // way; of 256 channels 743 and 824, and 8 x 1 row against 8192 51 and 75.  With fewer groups the other
-    // way is faster by up to 6 %.)
+    // way is faster by up to 6 %.  These 348, 743 and 51 were measured without the look at the scales; with it
+    // they are 358, 768 and 51.)
     constexpr bool ASK_FIRST = NG * NQ > 4;
     auto block = [&](bool asked, const uint8_t *x, int t0, bool ok) {
         int ln = lane;                                     // (of many groups: what comes from it is not kept in
@@ -847,10 +851,15 @@ Kv4AttendPlan kv4_attend_plan(int T, int max_new, int B, int q_heads, int heads,
         n = n < some * most ? n : some * most;
         // (joining them costs 5 us: not for fewer than two parts each of few tokens; 64 sequences
         // that see 1000 tokens each take 36 us in 96 parts, 26.5 whole.  Of many tokens a
-        // sequence may be far longer than the others.)
-        // Few tokens: eight waves are through with them before four and a second kernel are, where they
-        // have a CU each (one sequence of 8 heads: 500 tokens 8.1 us, 10.9 in parts; 1000 12.1 and
-        // 13.5, of it 12.0 on the GPU; 1500 15.2 and 13.1.  Four waves: 8.4, 13.4).
+        // sequence may be far longer than the others: the table's width is all that is known here, and
+        // these 64 take 31 us instead of 21 where it has room for more than 4096.)
+        // Few tokens: eight waves against four in parts and a second kernel, where the workgroups have a
+        // CU each.  1, 4, 16 and 32 sequences of 8 heads of 128, us in a graph, eight waves and parts: 768
+        // tokens 9.7/10.8, 9.8/11.0, 9.9/13.7, 10.3/16.6; 1024 11.1/10.8, 11.2/11.1, 11.4/13.8,
+        // 11.8/18.1; 1280 12.4/10.8, 12.7/11.1, 12.9/15.4, 13.3/19.7; 1536 14.0/10.8, 14.3/11.1,
+        // 14.6/15.6, 14.8/21.2.  Called one by one the second kernel and its workspace cost the host
+        // more: 14.7 at every length, and eight waves are faster up to 1536.  The border lies between the
+        // two ways of calling.
         const bool eight = D < 256 && likely <= 256 && tokens <= 1280;
         if (eight) p.shared = 8;
         if (!eight && may_join && (n >= 2 * some || (n > some && tokens > 4096))) {
